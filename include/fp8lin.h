@@ -22,7 +22,9 @@
  *   fp8_block_linear and fp8_sparse24_linear from three tokens on quantize
  *   the tokens into M * K + 4 * M * K / 128 bytes (and may split K as above);
  *   fp8_block_gemm_swiglu with few tokens keeps the fp32 partials of the
- *   stacked GEMM (S * M * 2I * 4 bytes).
+ *   stacked GEMM (S * M * 2I * 4 bytes);
+ *   paged_decode_attention and its _fp8 form keep fp32 partials of the
+ *   sequences that they split.
  * The scratch memory is held per device, stream and capture:
  *   - outside stream capture, one buffer per stream, from a stream-ordered
  *     pool the library creates once per device (hipMallocFromPoolAsync on
@@ -55,6 +57,7 @@
  *                    dimension above 2^24, or a matrix above 2^36 elements
  *                    (and M > 64 for the two *_linear calls);
  *                    for fp8_block_gemm_swiglu I plays the part of N;
+ *                    the decoder-layer calls state their own limits;
  *   FP8L_ERR_ALIGN   a pointer is not 16-byte aligned;
  *   FP8L_ERR_ALIAS   an output overlaps an input or another output;
  *   FP8L_ERR_DEVICE  the current HIP device is missing or is not gfx950;
@@ -371,6 +374,107 @@ fp8l_status fp8_block_linear(const uint16_t *x, const uint8_t *wq, const float *
  */
 fp8l_status fp8_sparse24_linear(const uint16_t *x, const uint8_t *wvals, const uint8_t *wmeta, const float *ws,
                                 int64_t M, int64_t N, int64_t K, uint16_t *y, hipStream_t stream);
+
+/*
+ * Decoder-layer operators between the FP8 linears: the residual norm that makes
+ * an FP8 linear's input, the append of a QKV projection's keys and values to a
+ * paged cache, and the attention of one new token over that cache.
+ *
+ * Paged cache.  k_cache and v_cache are [pages, Hkv, page_size, D]: the lines of
+ * one head of one page lie together.  Line `off` of page p is slot
+ * p * page_size + off.  bf16 values, or (the _fp8 calls) e4m3 codes with one
+ * fp32 scale amax / 448 for each token and head in k_scale and v_scale
+ * [pages, Hkv, page_size].
+ *   1 <= Hq, Hkv <= 1024; D is 64, 128 or 256; page_size a multiple of 16 up to
+ *   65536; pages * page_size < 2^31; pages * page_size * Hkv * D <= 2^40.
+ */
+
+/*
+ * Residual addition, root-mean-square norm and e4m3 quantization.
+ *
+ *   x [M,K] bf16, res [M,K] bf16 or NULL, w [K] bf16, 0 <= eps < inf
+ *   h [M,K] bf16     h = bf16_rne(x + res), the new residual stream: required
+ *                    with res, NULL without.  h == res updates it in place.
+ *   y [M,K] bf16     bf16_rne(v), or NULL, where (in fp32, h not rounded)
+ *                    v = (x + res) / sqrt(mean_k (x + res)^2 + eps) * w
+ *   q, s             codes and scales of v in 1x128 groups as in fp8_quant_act,
+ *                    from v in fp32 (not rounded to bf16 first): s = fp32(amax /
+ *                    448), q = enc(fp32(v / s)); both NULL: not produced
+ * The _ue8m0 call gives UE8M0 scale bytes as fp8_quant_act_ue8m0 does.  A group
+ * with an infinity or a NaN gets a non-finite scale (UE8M0: the NaN byte 0xFF).
+ * FP8L_ERR_NULL when exactly one of res and h, or of q and s, is NULL, or both
+ * y and q are; FP8L_ERR_SHAPE for an eps out of range.
+ */
+fp8l_status fp8_add_rmsnorm(const uint16_t *x, const uint16_t *res, const uint16_t *w, float eps, int64_t M,
+                            int64_t K, uint16_t *h, uint16_t *y, uint8_t *q, float *s, hipStream_t stream);
+fp8l_status fp8_add_rmsnorm_ue8m0(const uint16_t *x, const uint16_t *res, const uint16_t *w, float eps, int64_t M,
+                                  int64_t K, uint16_t *h, uint16_t *y, uint8_t *q, uint8_t *e, hipStream_t stream);
+
+/*
+ * Rotary position embedding of a QKV projection's output, and the append of its
+ * keys and values to the paged cache.
+ *
+ *   qkv [T, (Hq + 2 Hkv) D] bf16   a row holds the query heads, the key heads,
+ *                                  the value heads (the y of fp8_block_gemm)
+ *   positions [T] int32            clamped to 0 .. max_pos - 1
+ *   slots [T] int64                the token's cache line; negative or past the
+ *                                  cache: the token is not stored (padding)
+ *   cos_sin [max_pos, rot] fp32    row p: rot / 2 cosines, then rot / 2 sines
+ *   q_out [T, Hq, D] bf16          rotated queries (of every token)
+ * The first rot values (a multiple of 16, 0 .. D) of each query and key head
+ * turn: the pair (a, b) becomes (a cos - b sin, b cos + a sin) in fp32, pair i
+ * being values (i, i + rot / 2), or (2i, 2i + 1) if interleaved is not 0.  The
+ * other values and the value heads are copied.  Each result is rounded once: to
+ * bf16, or for the _fp8 call to codes with a scale for each token and head.
+ * Two tokens of one call must not have the same slot (which one stays is
+ * unspecified).  With rot == 0 positions and cos_sin are not read (may be NULL).
+ */
+fp8l_status kv_rope_append(const uint16_t *qkv, const int32_t *positions, const int64_t *slots, const float *cos_sin,
+                           int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved,
+                           int64_t max_pos, int64_t pages, int64_t page_size, uint16_t *q_out, uint16_t *k_cache,
+                           uint16_t *v_cache, hipStream_t stream);
+fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, const int64_t *slots,
+                               const float *cos_sin, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot,
+                               int interleaved, int64_t max_pos, int64_t pages, int64_t page_size, uint16_t *q_out,
+                               uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+                               hipStream_t stream);
+
+/*
+ * Attention of one new token of each of B sequences over the paged cache.
+ *
+ *   q [B,Hq,D] bf16                  Hq a multiple of Hkv: query head n reads
+ *                                    key head n / (Hq / Hkv)
+ *   block_table [B,max_pages] int32  page of tokens i page_size .. of sequence b
+ *                                    at [b,i]; entries past its length are not used
+ *   seq_lens [B] int32               tokens in the cache, the new one included;
+ *                                    clamped to 0 .. max_len
+ *   max_len                          a bound on seq_lens known to the host,
+ *                                    0 .. max_pages * page_size; sizes the launch
+ *   scale, softcap, window           score = scale (q . k); with softcap > 0,
+ *                                    softcap tanh(score / softcap); with window >
+ *                                    0 only the last `window` tokens count
+ *   o [B,Hq,D] bf16                  sum_t softmax(score)_t v_t
+ *   lse [B,Hq] fp32 or NULL          log sum_t exp(score_t), natural logarithm
+ * A sequence of length 0, or whose scores are all -inf, gives o = 0 and lse =
+ * -inf.  Scores, softmax sums and
+ * o are held in fp32; the softmax weights enter the product with v as two bf16
+ * numbers each (17 bits).  Cache lines past a sequence's length or before its
+ * window may hold anything.  Page numbers out of range are clamped: such rows
+ * are unspecified, with no access outside the cache.  Long sequences are split
+ * over workgroups, with fp32 partials in library scratch memory that a second
+ * kernel joins in a fixed order: results are deterministic.  B <= 65535.
+ */
+fp8l_status paged_decode_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                                   const int32_t *block_table, const int32_t *seq_lens, int64_t B, int64_t Hq,
+                                   int64_t Hkv, int64_t D, int64_t pages, int64_t page_size, int64_t max_pages,
+                                   int64_t max_len, float scale, float softcap, int64_t window, uint16_t *o,
+                                   float *lse, hipStream_t stream);
+fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                                       const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                       const int32_t *seq_lens, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                       int64_t pages, int64_t page_size, int64_t max_pages, int64_t max_len,
+                                       float scale, float softcap, int64_t window, uint16_t *o, float *lse,
+                                       hipStream_t stream);
 
 /*
  * Frees the scratch memory the library keeps for calls made under stream

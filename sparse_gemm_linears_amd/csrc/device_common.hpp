@@ -194,6 +194,49 @@ __device__ __forceinline__ uint32_t quantize4_group(const float (&x)[4], const G
   return g.fast ? quantize4_corrected(x, g) : quantize4_exact(x, g.s);
 }
 
+// Codes of eight fp32 values of a group whose largest magnitude has the fp32
+// bits amax, and the group's scale s = amax / 448 (an IEEE division): the codes
+// of fl(v / s).  With rs = fl(1 / s), the product v rs is within two ulp of the
+// quotient; one fused correction brings it within one ulp (the remainder
+// q s - v is exact or its error negligible) and a second one then rounds
+// correctly, because rs is a correctly rounded reciprocal.  Remainders stay
+// normal for amax >= 2^-60 wherever the code is not zero; smaller, zero and
+// non-finite amax take the IEEE divisions.
+__device__ __forceinline__ uint2 quantize8_f32(const float (&v)[8], uint32_t amax_f32_bits, float &s) {
+  s = __uint_as_float(amax_f32_bits) / 448.0f;
+  float q[8];
+  if (__builtin_expect(amax_f32_bits >= 0x21800000u && amax_f32_bits < 0x7F800000u, 1)) {
+    const float rs = 1.0f / s;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const float q0 = v[j] * rs;
+      const float r0 = __builtin_fmaf(q0, s, -v[j]);
+      const float q1 = __builtin_fmaf(-r0, rs, q0);
+      const float r1 = __builtin_fmaf(q1, s, -v[j]);
+      q[j] = __builtin_fmaf(-r1, rs, q1);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++) q[j] = s == 0.0f ? v[j] : v[j] / s;
+  }
+  return make_uint2(e4m3_pack4(q[0], q[1], q[2], q[3]), e4m3_pack4(q[4], q[5], q[6], q[7]));
+}
+
+// Eight bf16 values packed in 16 bytes, as fp32, and back (rounded to nearest even).
+__device__ __forceinline__ void unpack8(const uint4 &raw, float (&f)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
 // Maximum over the 16 lanes of a DPP row (lanes 16r .. 16r+15), in every lane
 // of the row: two quad permutations, then rotations of the row by 4 and 8.
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {

@@ -1,0 +1,216 @@
+// Residual addition, root-mean-square norm and e4m3 quantization of one row:
+//   h = x + res,  y = h / sqrt(mean(h^2) + eps) * w,
+//   codes and scale of each 128 channels of y.
+//
+// One pass over HBM: a row is held in fp32 registers between the sum of
+// squares and the output, so x and res are read once and h, the codes and the
+// scales written once (7.03 bytes per element with a residual).  HBM-bound
+// for many rows; one row is bound by two memory latencies and the launch.
+//
+// Numbers: h is exact in fp32 up to one rounding; the sum of squares is taken
+// in fp32 over the unrounded h, each lane's elements in order and the lanes in
+// a fixed tree, so results are deterministic.  y is not rounded to bf16 before
+// it is quantized: each code is one rounding of an fp32 value.
+#include "device_common.hpp"
+#include "launch_layer.hpp"
+
+namespace fp8lin {
+namespace {
+
+// Sum over the wave's 64 lanes in a fixed order, in every lane: four steps
+// inside each DPP row, then the four row sums.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto add = [](float x, int moved) { return x + __int_as_float(moved); };
+  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
+  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));  // row_ror 4
+  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));  // row_ror 8
+  const float r0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+  const float r1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+  const float r2 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
+  const float r3 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+  return (r0 + r1) + (r2 + r3);
+}
+
+__device__ __forceinline__ uint4 ld16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// Output of eight values of one row at column 8c: y, and the codes and scale
+// of the group that this lane and its 15 neighbours (one DPP row) hold.  The
+// 16 lanes are all active or all inactive, because K is a multiple of 128.
+__device__ __forceinline__ void emit8(const NormArgs &a, ScaleKind kind, int64_t row, int c, const float (&v)[8]) {
+  const int64_t at = row * a.K + 8 * (int64_t)c;
+  if (a.y) *reinterpret_cast<uint4 *>(a.y + at) = pack8(v);
+  if (!a.q) return;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  m = row16_max(m);
+  uint2 codes;
+  const int64_t group = row * (a.K / kGroup) + (c >> 4);
+  if (kind == ScaleKind::kUe8m0) {
+    // a group with an infinity or a NaN gets the scale byte that stands for NaN
+    const bool finite = m < 0x7F800000u;
+    const uint32_t e = finite ? ue8m0_exponent(m) : 255u;
+    const float inv = finite ? ue8m0_inverse(e) : 0.0f;
+    codes = make_uint2(e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                       e4m3_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    if ((c & 15) == 0) static_cast<uint8_t *>(a.scales)[group] = (uint8_t)e;
+  } else {
+    float s;
+    codes = quantize8_f32(v, m, s);
+    if ((c & 15) == 0) static_cast<float *>(a.scales)[group] = s;
+  }
+  *reinterpret_cast<uint2 *>(a.q + at) = codes;
+}
+
+// TEAM threads hold one row, V chunks of eight elements each (K <= 8 TEAM V).
+template <int TEAM, int V>
+__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rmsnorm_kernel(NormArgs a, ScaleKind kind) {
+  constexpr int kRows = TEAM < 256 ? 256 / TEAM : 1;
+  constexpr int kWaves = TEAM / 64;
+  const int t = threadIdx.x % TEAM;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TEAM;
+  if (row >= a.M) return;  // whole waves, and only in the one-wave form, which has no barrier
+  const int chunks = a.K / 8;
+  const int64_t base = row * a.K;
+  uint4 xr[V], wr[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    const int c = i * TEAM + t;
+    xr[i] = ld16(a.x + base + 8 * (int64_t)(c < chunks ? c : 0));
+  }
+  float h[V][8];
+  if (a.res) {
+    uint4 rr[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int c = i * TEAM + t;
+      rr[i] = ld16(a.res + base + 8 * (int64_t)(c < chunks ? c : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int c = i * TEAM + t;
+      wr[i] = ld16(a.w + 8 * (c < chunks ? c : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      float r[8];
+      unpack8(xr[i], h[i]);
+      unpack8(rr[i], r);
+#pragma unroll
+      for (int j = 0; j < 8; j++) h[i][j] += r[j];
+      const int c = i * TEAM + t;
+      if (c < chunks) *reinterpret_cast<uint4 *>(a.h + base + 8 * (int64_t)c) = pack8(h[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int c = i * TEAM + t;
+      wr[i] = ld16(a.w + 8 * (c < chunks ? c : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) unpack8(xr[i], h[i]);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    float part = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) part = __builtin_fmaf(h[i][j], h[i][j], part);
+    ss += i * TEAM + t < chunks ? part : 0.f;
+  }
+  ss = wave_sum(ss);
+  if constexpr (kWaves > 1) {
+    __shared__ float wave_ss[kWaves];
+    if ((t & 63) == 0) wave_ss[t >> 6] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; i++) ss += wave_ss[i];
+  }
+  const float rinv = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    const int c = i * TEAM + t;
+    if (c >= chunks) continue;
+    float w[8];
+    unpack8(wr[i], w);
+#pragma unroll
+    for (int j = 0; j < 8; j++) h[i][j] = h[i][j] * rinv * w[j];
+    emit8(a, kind, row, c, h[i]);
+  }
+}
+
+// Rows longer than the register forms hold: two passes over the row, the
+// second from the caches where it fits them.  h is written in the second pass
+// only, because it may be the same memory as res.
+__global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a, ScaleKind kind) {
+  __shared__ float wave_ss[16];
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x, base = row * a.K;
+  const int chunks = a.K / 8;
+  auto load = [&](int c, float (&h)[8]) {
+    unpack8(ld16(a.x + base + 8 * (int64_t)c), h);
+    if (a.res) {
+      float r[8];
+      unpack8(ld16(a.res + base + 8 * (int64_t)c), r);
+#pragma unroll
+      for (int j = 0; j < 8; j++) h[j] += r[j];
+    }
+  };
+  float ss = 0.f;
+  for (int c = t; c < chunks; c += 1024) {
+    float h[8], part = 0.f;
+    load(c, h);
+#pragma unroll
+    for (int j = 0; j < 8; j++) part = __builtin_fmaf(h[j], h[j], part);
+    ss += part;
+  }
+  ss = wave_sum(ss);
+  if ((t & 63) == 0) wave_ss[t >> 6] = ss;
+  __syncthreads();
+  ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i++) ss += wave_ss[i];
+  const float rinv = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  for (int c = t; c < chunks; c += 1024) {
+    float h[8], w[8];
+    load(c, h);
+    unpack8(ld16(a.w + 8 * (int64_t)c), w);
+    if (a.res) *reinterpret_cast<uint4 *>(a.h + base + 8 * (int64_t)c) = pack8(h);
+#pragma unroll
+    for (int j = 0; j < 8; j++) h[j] = h[j] * rinv * w[j];
+    emit8(a, kind, row, c, h);
+  }
+}
+
+template <int TEAM, int V>
+void launch_rows(const NormArgs &a, ScaleKind kind, hipStream_t stream) {
+  constexpr int kRows = TEAM < 256 ? 256 / TEAM : 1;
+  hipLaunchKernelGGL((rmsnorm_kernel<TEAM, V>), dim3((unsigned)((a.M + kRows - 1) / kRows)),
+                     dim3(TEAM < 256 ? 256 : TEAM), 0, stream, a, kind);
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const NormArgs &a, ScaleKind kind, hipStream_t stream) {
+  if (a.K <= 512)
+    launch_rows<64, 1>(a, kind, stream);
+  else if (a.K <= 1024)
+    launch_rows<64, 2>(a, kind, stream);
+  else if (a.K <= 2048)
+    launch_rows<256, 1>(a, kind, stream);
+  else if (a.K <= 4096)
+    launch_rows<256, 2>(a, kind, stream);
+  else if (a.K <= 8192)
+    launch_rows<256, 4>(a, kind, stream);
+  else if (a.K <= 16384)
+    launch_rows<512, 4>(a, kind, stream);
+  else if (a.K <= 32768)
+    launch_rows<1024, 4>(a, kind, stream);
+  else
+    hipLaunchKernelGGL(rmsnorm_long_kernel, dim3((unsigned)a.M), dim3(1024), 0, stream, a, kind);
+  return hipGetLastError();
+}
+
+}  // namespace fp8lin
