@@ -449,7 +449,7 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  *   seq_lens [B] int32               tokens in the cache, the new one included;
  *                                    clamped to 0 .. max_len
  *   max_len                          a bound on seq_lens known to the host,
- *                                    0 .. max_pages * page_size; sizes the launch
+ *                                    0 .. max_pages * page_size (<= 2^30)
  *   scale, softcap, window           score = scale (q . k); with softcap > 0,
  *                                    softcap tanh(score / softcap); with window >
  *                                    0 only the last `window` tokens count
@@ -460,9 +460,11 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  * o are held in fp32; the softmax weights enter the product with v as two bf16
  * numbers each (17 bits).  Cache lines past a sequence's length or before its
  * window may hold anything.  Page numbers out of range are clamped: such rows
- * are unspecified, with no access outside the cache.  Long sequences are split
- * over workgroups, with fp32 partials in library scratch memory that a second
- * kernel joins in a fixed order: results are deterministic.  B <= 65535.
+ * are unspecified, with no access outside the cache.  Where max_len is more than
+ * 512 tokens the whole batch's tokens are divided evenly over the workgroups,
+ * with fp32 partials in library scratch memory that a second kernel joins in a
+ * fixed order: results are deterministic, but a row's rounding depends on the
+ * lengths beside it.  B <= 65535.
  */
 fp8l_status paged_decode_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                                    const int32_t *block_table, const int32_t *seq_lens, int64_t B, int64_t Hq,

@@ -15,6 +15,7 @@ using namespace fp8lin;  // the shared checks
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxPage = 65536;
 constexpr int64_t kMaxSlots = (int64_t(1) << 31) - 1;  // cache lines of one head: pages * page_size
+constexpr int64_t kMaxTokens = int64_t(1) << 30;          // of one sequence: max_pages * page_size
 constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxCacheElems = int64_t(1) << 40;
 
@@ -82,7 +83,7 @@ fp8l_status decode(const DecodeArgs &in, int64_t B, int64_t Hq, int64_t Hkv, int
                    int64_t page_size, int64_t max_pages, int64_t max_len, int64_t window, bool fp8,
                    hipStream_t stream) {
   if (bad_cache(Hq, Hkv, D, pages, page_size) || Hq % Hkv != 0 || B < 0 || B > kMaxBatch || max_pages <= 0 ||
-      max_pages > kMaxSlots || max_pages * page_size > kMaxSlots || max_len < 0 || max_len > max_pages * page_size ||
+      max_pages > kMaxTokens || max_pages * page_size > kMaxTokens || max_len < 0 || max_len > max_pages * page_size ||
       window < 0 || !std::isfinite(in.scale) || !(in.softcap >= 0.0f) || std::isinf(in.softcap))
     return FP8L_ERR_SHAPE;
   if (B == 0) return FP8L_OK;

@@ -12,10 +12,16 @@
 // the query heads of one key head (unused ones are zero), and the softmax
 // weights enter the second product as two bf16 numbers each.
 //
-// A workgroup takes one key head, up to 16 RT of its query heads and `chunk`
-// tokens; its waves take 32-token tiles in turn, each with a softmax state of
-// its own, joined through LDS.  Sequences longer than a chunk leave fp32 partials that
-// join_kernel adds in chunk order.
+// A row is one key head of one sequence with up to 16 RT of its query heads, and
+// work is counted in tiles of 32 tokens.  Lengths are known on the device only,
+// and a grid made for the longest sequence leaves most of it without work in a
+// ragged batch.  So a fixed number of waves divides all tiles of the batch into
+// even shares: each finds its share from the lengths and takes the rows in it in
+// turn, the next tile always loading while one is used.  Waves work alone: no
+// barrier, no LDS.  A wave leaves a partial for the row that its share begins
+// inside and for the one that it ends inside; join_kernel adds the partials of a
+// row in order.  One sequence alone, and batches that give each wave a tile at
+// most, are divided by the grid, without the search.
 //
 // Layouts (v_mfma_f32_16x16x32_bf16: lane l, n = l % 16, g = l / 16):
 //   scores   A = K: row n is token n of a half tile, B = Q: column n is a query
@@ -41,6 +47,7 @@ constexpr int kTile = 32;  // tokens of a wave's tile
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ v8bf as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(v8bf, (v4u{a, b, c, d}));
@@ -93,13 +100,13 @@ __device__ __forceinline__ void load_tile(Tile<D, FP8> &t, const DecodeArgs &a, 
     if constexpr (T::kV == 1) {
       t.v[j][0] = *reinterpret_cast<const uint32_t *>(vp + at);
     } else if constexpr (T::kV == 2) {
-      const uint2 x = *reinterpret_cast<const uint2 *>(vp + at);
-      t.v[j][0] = x.x;
-      t.v[j][1] = x.y;
+      const v2u x = __builtin_nontemporal_load(reinterpret_cast<const v2u *>(vp + at));
+      t.v[j][0] = x[0];
+      t.v[j][1] = x[1];
     } else {
 #pragma unroll
       for (int c = 0; c < T::kV / 4; c++) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(vp + (at + 16 * c));
+        const uint4 x = ldg16_stream(vp + (at + 16 * c));
         t.v[j][4 * c] = x.x;
         t.v[j][4 * c + 1] = x.y;
         t.v[j][4 * c + 2] = x.z;
@@ -249,249 +256,424 @@ __device__ __forceinline__ void use_tile(Tile<D, FP8> &t, const DecodeArgs &a, c
   }
 }
 
-// Partials of one (sequence, chunk): o [Hq][D], then m and l [Hq] each.
-__host__ __device__ inline size_t partial_floats(int Hq, int D) { return (size_t)Hq * (D + 2); }
+constexpr int kWaves = 4;  // of a workgroup; each works alone
+constexpr int kThreads = 64 * kWaves;
+constexpr int kListed = 64;  // tiles that a wave lists at a time, one in each lane
 
 __host__ __device__ inline int first_token(int len, int window) {
   const int lo = window > 0 && len > window ? len - window : 0;
   return lo & ~(kTile - 1);
 }
 
-// Whether a wave loads its next tile before it uses the present one: where two
-// tiles and the state fit the registers of two waves on a SIMD (or one, for D = 256).
-template <int D, int RT>
-constexpr bool kAhead = D * RT <= 128 || RT == 1;
-
-template <int D, bool FP8, int RT, int NW>
-__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void decode_kernel(DecodeArgs a, int chunk, int splits, float *part) {
-  constexpr int kPad = D + 4;  // a row of LDS, off the bank period
-  extern __shared__ __align__(16) char lds[];
-  int64_t *lines = reinterpret_cast<int64_t *>(lds);  // first cache line of each half tile
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT);
-  const int kvh = blockIdx.y / bands, head0 = (blockIdx.y % bands) * 16 * RT;
-  const int heads = min(group - head0, 16 * RT);  // query heads of this workgroup
-  const int64_t q0 = (int64_t)b * a.Hq + kvh * group + head0;
-  const int len = min(max(a.seq_lens[b], 0), a.max_len);
-  const int lo = a.window > 0 ? max(0, len - a.window) : 0;
-  const int begin = first_token(len, a.window) + split * chunk;
-  const int end = min(len, begin + chunk);
-  if (begin >= end && !(split == 0)) return;  // chunks past the sequence; the first one writes its zeros
-  const int halves = begin < end ? (end - begin + 15) / 16 : 0;
-  for (int i = threadIdx.x; i < (halves + 1) / 2 * 2; i += 64 * NW) {
-    const int token = begin + 16 * min(i, halves - 1);  // the odd last half tile repeats, its tokens are dead
-    const int at = token / a.page_size;
-    const int page = min(max(a.block_table[(int64_t)b * a.max_pages + at], 0), a.pages - 1);
-    lines[i] = ((int64_t)page * a.Hkv + kvh) * a.page_size + (token - at * a.page_size);
-  }
-  v8bf qf[RT][D / 32];
-#pragma unroll
-  for (int r = 0; r < RT; r++) {
-#pragma unroll
-    for (int c = 0; c < D / 32; c++) {
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (16 * r + n < heads)
-        raw = *reinterpret_cast<const uint4 *>(a.q + (q0 + 16 * r + n) * D + 64 * (c >> 1) + 16 * g + 8 * (c & 1));
-      qf[r][c] = as_bf16x8(raw.x, raw.y, raw.z, raw.w);
-    }
-  }
-  State<D> st[RT];
-#pragma unroll
-  for (int r = 0; r < RT; r++) {
-    st[r].m = -INFINITY;
-    st[r].l = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 16; i++) st[r].o[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  }
-  __syncthreads();
-  const int tiles = (halves + 1) / 2;
-  auto load = [&](Tile<D, FP8> &t, int i) {
-    int64_t line[2];
-#pragma unroll
-    for (int hh = 0; hh < 2; hh++) {
-      const int64_t x = lines[2 * i + hh];
-      line[hh] = (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) |
-                 (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
-    }
-    load_tile<D, FP8>(t, a, line, n, g);
-  };
-  Tile<D, FP8> ta;
-  if constexpr (kAhead<D, RT>) {
-    Tile<D, FP8> tb;
-    int i = wave;
-    if (i < tiles) load(ta, i);
-    while (i < tiles) {
-      if (i + NW < tiles) load(tb, i + NW);
-      use_tile<D, FP8, RT>(ta, a, qf, st, begin + kTile * i, lo, end, g);
-      i += NW;
-      if (i >= tiles) break;
-      if (i + NW < tiles) load(ta, i + NW);
-      use_tile<D, FP8, RT>(tb, a, qf, st, begin + kTile * i, lo, end, g);
-      i += NW;
-    }
-  } else {
-    for (int i = wave; i < tiles; i += NW) {
-      load(ta, i);
-      use_tile<D, FP8, RT>(ta, a, qf, st, begin + kTile * i, lo, end, g);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; r++) {
-    st[r].l += __shfl_xor(st[r].l, 16, 64);
-    st[r].l += __shfl_xor(st[r].l, 32, 64);
-  }
-  // join the waves' states pairwise, in a fixed order, through LDS
-  float *box_o = reinterpret_cast<float *>(lds);
-  float *box_m = box_o + NW / 2 * 16 * RT * kPad, *box_l = box_m + NW / 2 * 16 * RT;
-#pragma unroll
-  for (int half = NW / 2; half >= 1; half /= 2) {
-    __syncthreads();
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int r = 0; r < RT; r++) {
-        const int row = (wave - half) * 16 * RT + 16 * r + n;
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-#pragma unroll
-          for (int e = 0; e < D / 16; e++) box_o[row * kPad + D / 16 * (4 * g + k) + e] = st[r].o[e][k];
-        }
-        if (g == 0) {
-          box_m[row] = st[r].m;
-          box_l[row] = st[r].l;
-        }
-      }
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int r = 0; r < RT; r++) {
-        const int row = wave * 16 * RT + 16 * r + n;
-        const float m2 = box_m[row], top = fmaxf(st[r].m, m2);
-        const float f1 = st[r].m == top ? 1.f : __builtin_amdgcn_exp2f(st[r].m - top);
-        const float f2 = m2 == top ? 1.f : __builtin_amdgcn_exp2f(m2 - top);
-        st[r].m = top;
-        st[r].l = st[r].l * f1 + box_l[row] * f2;
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-#pragma unroll
-          for (int e = 0; e < D / 16; e++)
-            st[r].o[e][k] = st[r].o[e][k] * f1 + box_o[row * kPad + D / 16 * (4 * g + k) + e] * f2;
-        }
-      }
-    }
-  }
-  if (wave != 0) return;
-#pragma unroll
-  for (int r = 0; r < RT; r++) {
-    const int head = 16 * r + n;
-    if (head >= heads) continue;
-    if (splits == 1) {
-      const float inv = st[r].l == 0.f ? 0.f : 1.f / st[r].l;
-      uint16_t *dst = a.o + (q0 + head) * D;
-#pragma unroll
-      for (int k = 0; k < 4; k++) {
-#pragma unroll
-        for (int e = 0; e < D / 16; e += 4)
-          *reinterpret_cast<uint2 *>(dst + D / 16 * (4 * g + k) + e) =
-              make_uint2(pack_bf16x2(st[r].o[e][k] * inv, st[r].o[e + 1][k] * inv),
-                         pack_bf16x2(st[r].o[e + 2][k] * inv, st[r].o[e + 3][k] * inv));
-      }
-      if (a.lse && g == 0) a.lse[q0 + head] = st[r].l == 0.f ? -INFINITY : kLn2 * (st[r].m + log2f(st[r].l));
-    } else {
-      float *base = part + ((size_t)b * splits + split) * partial_floats(a.Hq, D);
-      const int at = kvh * group + head0 + head;
-#pragma unroll
-      for (int k = 0; k < 4; k++) {
-#pragma unroll
-        for (int e = 0; e < D / 16; e += 4)
-          *reinterpret_cast<float4 *>(base + (size_t)at * D + D / 16 * (4 * g + k) + e) =
-              make_float4(st[r].o[e][k], st[r].o[e + 1][k], st[r].o[e + 2][k], st[r].o[e + 3][k]);
-      }
-      if (g == 0) {
-        base[(size_t)a.Hq * D + at] = st[r].m;
-        base[(size_t)a.Hq * (D + 1) + at] = st[r].l;
-      }
-    }
-  }
+__device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
+  return b < a.B ? min(max(a.seq_lens[b], 0), a.max_len) : 0;
 }
 
-// Joins the chunks of one query head, in chunk order.
-template <int D>
-__global__ __launch_bounds__(64) void join_kernel(DecodeArgs a, int chunk, int splits, const float *part) {
-  constexpr int E = D / 64;
-  const int head = blockIdx.x, b = blockIdx.y, lane = threadIdx.x;
-  const int len = min(max(a.seq_lens[b], 0), a.max_len);
-  const int live = max(1, (len - first_token(len, a.window) + chunk - 1) / chunk);
-  const size_t stride = partial_floats(a.Hq, D);
-  const float *base = part + (size_t)b * splits * stride;
-  float top = -INFINITY;
-  for (int s = lane; s < live; s += 64) top = fmaxf(top, base[s * stride + (size_t)a.Hq * D + head]);
-  for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  float l = 0.f, o[E] = {};
-  for (int s = 0; s < live; s++) {
-    const float *p = base + s * stride;
-    const float m = p[(size_t)a.Hq * D + head];
-    const float f = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
-    l += p[(size_t)a.Hq * (D + 1) + head] * f;
-#pragma unroll
-    for (int e = 0; e < E; e++) o[e] += p[(size_t)head * D + E * lane + e] * f;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = (int64_t)b * a.Hq + head;
-#pragma unroll
-  for (int e = 0; e < E; e++) a.o[at * D + E * lane + e] = (uint16_t)f32_to_bf16_rne(o[e] * inv);
-  if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+// Tiles of a sequence (an empty one has a tile without live tokens, which
+// writes its zeros).
+__device__ __forceinline__ int tiles_of(const DecodeArgs &a, int len) {
+  return max(1, (len - first_token(len, a.window) + kTile - 1) / kTile);
 }
 
-constexpr int kWaves = 4;
-
-// Tokens of a chunk and the chunks of the longest sequence: enough workgroups
-// to cover the compute units a few times, in whole rounds of the waves' tiles.
+// How work is divided.  per == 0: even shares; the rows of a sequence follow
+// each other (bands of query heads within a key head), and wave i of
+// 2^log2_parts takes tiles share_start(i) .. share_start(i + 1) - 1 of all.
+// per > 0: each row has `splits` waves of `per` tiles.
 struct Plan {
-  int chunk, splits;
+  int per, splits, log2_parts;
+  int waves;
+  int64_t rows;  // of the batch
+  bool by_row;   // whether the list of divided rows is indexed by row, or by share
 };
 
+__device__ __forceinline__ int64_t share_start(int64_t i, int64_t total, int log2_parts) {
+  const int64_t parts = (int64_t)1 << log2_parts;
+  return total <= parts ? (i < total ? i : total) : i * total >> log2_parts;
+}
+
+// A row that is divided (slot < 0: none): its parts are in `slot` and in slot 0 of
+// the waves that follow `owner`: `parts` of them in all, or (parts == 0) as many
+// as have shares that start before row_end.
+struct Cut {
+  int64_t total, row_end;
+  int b, band, slot, parts;
+  int owner, pad;
+};
+
+// Partials of one part of a row: o [16 RT][D], then m and l [16 RT] each.  Each
+// wave has two slots.
+__host__ __device__ constexpr size_t part_floats(int D, int RT) { return (size_t)16 * RT * (D + 2); }
+
+// A tile of the batch: the tile `tile` of row `band` of sequence b.
+struct Place {
+  int b, band, tile, len;
+};
+
+// All tiles of the batch; before and upto: those of the sequences before this
+// lane's run of sequences, and with it.
+__device__ __forceinline__ int64_t batch_tiles(const DecodeArgs &a, int rows, int lane, int64_t &before,
+                                               int64_t &upto) {
+  const int per = (a.B + 63) / 64, b0 = lane * per, b1 = min(a.B, b0 + per);
+  int64_t mine = 0;
+  for (int i = b0; i < b1; i++) mine += tiles_of(a, length_of(a, i));
+  mine *= rows;
+  upto = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t x = __shfl_up(upto, off, 64);
+    if (lane >= off) upto += x;
+  }
+  before = upto - mine;
+  return __shfl(upto, 63, 64);
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int from_lane(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
+  return (int64_t)(uint32_t)from_lane((int)x, lane) | (int64_t)from_lane((int)(x >> 32), lane) << 32;
+}
+
+// Quotient of a tile's place among a sequence's tiles by the tiles of a row.
+__device__ __forceinline__ int row_of(int64_t inside, int tiles) {
+  return inside >> 31 ? (int)(inside / tiles) : (int)((uint32_t)inside / (uint32_t)tiles);
+}
+
+__device__ __forceinline__ Place find_tile(const DecodeArgs &a, int rows, int lane, int64_t at, int64_t before,
+                                           int64_t upto) {
+  const int per = (a.B + 63) / 64, b0 = lane * per, b1 = min(a.B, b0 + per);
+  int b = 0, band = 0, tile = 0, len = 0;
+  const bool mine = at >= before && at < upto;
+  if (mine) {
+    b = b0;
+    len = length_of(a, b);
+    int64_t inside = at - before;
+    for (int64_t n; b + 1 < b1 && inside >= (n = (int64_t)tiles_of(a, len) * rows); inside -= n) len = length_of(a, ++b);
+    const int tiles = tiles_of(a, len);
+    band = row_of(inside, tiles);
+    tile = (int)(inside - (int64_t)band * tiles);
+  }
+  const int src = __ffsll((unsigned long long)__ballot(mine)) - 1;
+  return Place{from_lane(b, src), from_lane(band, src), from_lane(tile, src), from_lane(len, src)};
+}
+
+template <int D, bool FP8, int RT>
+__global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void decode_kernel(DecodeArgs a, Plan plan, float *part,
+                                                                           Cut *cuts) {
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int self = uniform((int)blockIdx.x * kWaves + (int)(threadIdx.x >> 6));
+  if (self >= plan.waves) return;
+  const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT), rows = a.Hkv * bands;
+
+  Place at;      // the next tile to list
+  int64_t left;  // tiles of the share that are not listed yet
+  int64_t total = 0, position = 0;  // tiles of the batch, and where the share starts in them
+  if (plan.per > 0) {
+    const int row = self / plan.splits, split = self - row * plan.splits;
+    at.b = row / rows;
+    at.band = row - at.b * rows;
+    at.tile = split * plan.per;
+    at.len = uniform(length_of(a, at.b));
+    left = min(plan.per, tiles_of(a, at.len) - at.tile);
+    if (left <= 0) return;
+  } else {
+    int64_t before, upto;
+    total = batch_tiles(a, rows, lane, before, upto);
+    position = share_start(self, total, plan.log2_parts);
+    left = share_start(self + 1, total, plan.log2_parts) - position;
+    if (!plan.by_row && lane == 0) cuts[self].slot = -1;
+    if (left <= 0) return;  // there are more waves than tiles
+    at = find_tile(a, rows, lane, position, before, upto);
+  }
+  bool started = true;        // whether this is the share's first row
+  int row_begin = at.tile;    // first tile of the present row that is in the share
+  int64_t row_position = position - at.tile;  // of the present row's first tile
+
+  v8bf qf[RT][D / 32];
+  auto load_q = [&](int b, int band) {
+    const int kvh = band / bands, head0 = (band - kvh * bands) * 16 * RT;
+    const int heads = min(group - head0, 16 * RT);
+    const uint16_t *src = a.q + ((int64_t)b * a.Hq + kvh * group + head0) * D;
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+#pragma unroll
+      for (int c = 0; c < D / 32; c++) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (16 * r + n < heads)
+          raw = *reinterpret_cast<const uint4 *>(src + (16 * r + n) * D + 64 * (c >> 1) + 16 * g + 8 * (c & 1));
+        qf[r][c] = as_bf16x8(raw.x, raw.y, raw.z, raw.w);
+      }
+    }
+  };
+  load_q(at.b, at.band);
+  State<D> st[RT];
+  auto clear = [&] {
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      st[r].m = -INFINITY;
+      st[r].l = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; i++) st[r].o[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  clear();
+
+  while (left > 0) {
+    // list the next tiles: lane x finds tile x and its cache lines
+    const int count = (int)min(left, (int64_t)kListed);
+    int rb = at.b, rband = at.band, rtile = at.tile + lane, rlen = at.len;
+    if (count > tiles_of(a, at.len) - at.tile) {  // they reach past the present row
+      const int len = length_of(a, at.b + lane), tiles = tiles_of(a, len);
+      // tiles of sequence at.b + lane from here on (more than 1024 are as good), and their running sum
+      const int64_t all = (int64_t)tiles * rows - (lane == 0 ? (int64_t)at.band * tiles + at.tile : 0);
+      int mine = at.b + lane < a.B ? (int)min(all, (int64_t)1024) : 0, upto = mine;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int x = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += x;
+      }
+      int s = 0;  // first sequence whose running sum passes the lane's number
+#pragma unroll
+      for (int step = 32; step; step >>= 1)
+        if (__shfl(upto, s + step - 1, 64) <= lane) s += step;
+      const int before = __shfl(upto - mine, s, 64);
+      const int stiles = __shfl(tiles, s, 64);
+      rlen = __shfl(len, s, 64);
+      rb = at.b + s;
+      const int64_t inside = lane - before + (s == 0 ? (int64_t)at.band * stiles + at.tile : 0);
+      rband = row_of(inside, stiles);
+      rtile = (int)(inside - (int64_t)rband * stiles);
+    }
+    const int rtoken = first_token(rlen, a.window) + rtile * kTile;
+    int64_t rline[2] = {0, 0};  // of tokens past the end, which count for nothing: any line will do
+    const int rkvh = rband / bands;
+#pragma unroll
+    for (int hh = 0; hh < 2; hh++) {
+      const int token = rtoken + 16 * hh;
+      if (lane < count && token < rlen) {
+        const int p = (int)((uint32_t)token / (uint32_t)a.page_size);
+        const int page = min(max(a.block_table[(int64_t)rb * a.max_pages + p], 0), a.pages - 1);
+        rline[hh] = ((int64_t)page * a.Hkv + rkvh) * a.page_size + (token - p * a.page_size);
+      }
+    }
+    // where the next list begins: one tile after the last of this one
+    at = Place{from_lane(rb, count - 1), from_lane(rband, count - 1), from_lane(rtile, count - 1) + 1,
+               from_lane(rlen, count - 1)};
+    left -= count;
+    if (left > 0 && at.tile == tiles_of(a, at.len)) {
+      at.tile = 0;
+      if (++at.band == rows) {
+        at.band = 0;
+        at.b++;
+        at.len = uniform(length_of(a, at.b));
+      }
+    }
+    auto load = [&](Tile<D, FP8> &t, int i) {
+      const int64_t line[2] = {from_lane(rline[0], i), from_lane(rline[1], i)};
+      load_tile<D, FP8>(t, a, line, n, g);
+    };
+    for (int i = 0; i < count; i++) {
+      const int token = from_lane(rtoken, i), len = from_lane(rlen, i);
+      Tile<D, FP8> now;
+      load(now, i);
+      use_tile<D, FP8, RT>(now, a, qf, st, token, a.window > 0 ? max(0, len - a.window) : 0, len, g);
+      const bool row_ends = token + kTile >= len, share_ends = i + 1 == count && left == 0;
+      if (row_ends || share_ends) {
+        const int b = from_lane(rb, i), band = from_lane(rband, i);
+        if (!share_ends)  // the next row's queries
+          load_q(i + 1 < count ? from_lane(rb, (i + 1) & 63) : at.b, i + 1 < count ? from_lane(rband, (i + 1) & 63) : at.band);
+        const int tiles = tiles_of(a, len);
+        const bool whole = row_begin == 0 && row_ends;
+        const int slot = 2 * self + (started ? 0 : 1);
+        const int kvh = band / bands, head0 = (band - kvh * bands) * 16 * RT;
+        const int heads = min(group - head0, 16 * RT);
+        const int64_t q0 = (int64_t)b * a.Hq + kvh * group + head0;
+#pragma unroll
+        for (int r = 0; r < RT; r++) {
+          const int head = 16 * r + n;
+          float l = st[r].l;
+          l += __shfl_xor(l, 16, 64);
+          l += __shfl_xor(l, 32, 64);
+          if (head >= heads) continue;
+          // this lane holds values D / 4 g .. + D / 4 - 1 of its head
+          if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint16_t *dst = a.o + (q0 + head) * D + D / 4 * g;
+#pragma unroll
+            for (int e = 0; e < D / 4; e += 8) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; k++) v[k] = st[r].o[(e + k) % (D / 16)][(e + k) / (D / 16)] * inv;
+              *reinterpret_cast<uint4 *>(dst + e) = pack8(v);
+            }
+            if (a.lse && g == 0) a.lse[q0 + head] = l == 0.f ? -INFINITY : kLn2 * (st[r].m + log2f(l));
+          } else {
+            float *base = part + slot * part_floats(D, RT), *dst = base + head * D + D / 4 * g;
+#pragma unroll
+            for (int e = 0; e < D / 4; e += 4) {
+              float v[4];
+#pragma unroll
+              for (int k = 0; k < 4; k++) v[k] = st[r].o[(e + k) % (D / 16)][(e + k) / (D / 16)];
+              *reinterpret_cast<float4 *>(dst + e) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            if (g == 0) {
+              base[16 * RT * D + head] = st[r].m;
+              base[16 * RT * (D + 1) + head] = l;
+            }
+          }
+        }
+        if (lane == 0 && row_begin == 0 && (plan.by_row || !whole)) {
+          const int parts = plan.per > 0 ? (tiles + plan.per - 1) / plan.per : 0;
+          cuts[plan.by_row ? (int64_t)b * rows + band : (int64_t)self] =
+              Cut{total, row_position + tiles, b, band, whole ? -1 : slot, parts, self, 0};
+        }
+        clear();
+        started = false;
+        row_begin = 0;
+        row_position += tiles;
+      }
+    }
+  }
+}
+
+// Joins the parts of a divided row, in a fixed order: workgroup (i, y) takes row
+// i of the list, and of its query heads y, y + gridDim.y, ...  Wave w adds parts
+// w, w + JW, ... with a running maximum (eight loads in flight), then the waves'
+// sums are added.  A part weighs 2^(m - top).
+template <int D, int RT, int JW>
+__global__ __launch_bounds__(64 * JW) void join_kernel(DecodeArgs a, int log2_parts, const float *part,
+                                                       const Cut *cuts) {
+  constexpr int E = D / 64;
+  __shared__ float wave_top[JW], wave_l[JW], wave_o[JW][D];
+  const Cut cut = cuts[blockIdx.x];
+  if (cut.slot < 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT);
+  const int kvh = cut.band / bands, head0 = (cut.band - kvh * bands) * 16 * RT;
+  const int heads = min(group - head0, 16 * RT);
+  int parts = cut.parts;
+  if (parts == 0) {
+    // shares from the owner's on that start before the row's end
+    int low = 1, high = (1 << log2_parts) - cut.owner;
+    while (low < high) {
+      const int mid = (low + high) / 2;
+      if (share_start((int64_t)cut.owner + mid, cut.total, log2_parts) < cut.row_end)
+        low = mid + 1;
+      else
+        high = mid;
+    }
+    parts = low;
+  }
+  for (int head = blockIdx.y; head < heads; head += gridDim.y) {
+    float top = -INFINITY, l = 0.f, o[E] = {};
+    for (int k0 = wave; k0 < parts; k0 += 8 * JW) {
+      float m[8], lp[8], op[8][E];
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        const int k = min(k0 + JW * u, parts - 1);
+        const float *p = part + (size_t)(k == 0 ? cut.slot : 2 * (cut.owner + k)) * part_floats(D, RT);
+        m[u] = k0 + JW * u < parts ? p[16 * RT * D + head] : -INFINITY;
+        lp[u] = p[16 * RT * (D + 1) + head];
+#pragma unroll
+        for (int e = 0; e < E; e++) op[u][e] = p[head * D + E * lane + e];
+      }
+      float high = top;
+#pragma unroll
+      for (int u = 0; u < 8; u++) high = fmaxf(high, m[u]);
+      const float shrink = top == high ? 1.f : __builtin_amdgcn_exp2f(top - high);
+      top = high;
+      l *= shrink;
+#pragma unroll
+      for (int e = 0; e < E; e++) o[e] *= shrink;
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        if (k0 + JW * u < parts) {
+          const float f = m[u] == top ? 1.f : __builtin_amdgcn_exp2f(m[u] - top);
+          l += lp[u] * f;
+#pragma unroll
+          for (int e = 0; e < E; e++) o[e] += op[u][e] * f;
+        }
+      }
+    }
+    __syncthreads();  // the boxes are free
+    if (lane == 0) {
+      wave_top[wave] = top;
+      wave_l[wave] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; e++) wave_o[wave][E * lane + e] = o[e];
+    __syncthreads();
+    const int64_t at = (int64_t)cut.b * a.Hq + kvh * group + head0 + head;
+    for (int d = threadIdx.x; d < D; d += 64 * JW) {
+      float high = -INFINITY, sum = 0.f, weight = 0.f;
+#pragma unroll
+      for (int w = 0; w < JW; w++) high = fmaxf(high, wave_top[w]);
+#pragma unroll
+      for (int w = 0; w < JW; w++) {
+        const float f = wave_top[w] == high ? 1.f : __builtin_amdgcn_exp2f(wave_top[w] - high);
+        weight += wave_l[w] * f;
+        sum += wave_o[w][d] * f;
+      }
+      a.o[at * D + d] = (uint16_t)f32_to_bf16_rne(weight == 0.f ? 0.f : sum / weight);
+      if (a.lse && d == 0) a.lse[at] = weight == 0.f ? -INFINITY : kLn2 * (high + log2f(weight));
+    }
+  }
+}
+
+// Sets of 16 query heads that a row holds: two where a key head has more than 16,
+// so that its lines are read once for up to 32 (not for D = 256, whose state of
+// two sets leaves no registers for the tiles).
+int row_tiles(const DecodeArgs &a) { return a.Hq / a.Hkv <= 16 || a.D == 256 ? 1 : 2; }
+
 Plan plan_decode(const DecodeArgs &a, int cus) {
-  const int round = kWaves * kTile;
-  // live tokens of a sequence, from the tile that holds the first one
-  int64_t tokens = a.max_len;
-  if (a.window > 0) tokens = tokens < (int64_t)a.window + kTile ? tokens : (int64_t)a.window + kTile;
-  if (tokens < 1) tokens = 1;
-  const int64_t rows = (int64_t)a.B * a.Hkv * ((a.Hq / a.Hkv + 15) / 16);
-  const int64_t want = (4 * (int64_t)cus + rows - 1) / rows;  // chunks of a sequence
-  int64_t chunk = (tokens + want - 1) / want;
-  chunk = (chunk + round - 1) / round * round;
-  if (chunk < 2 * round) chunk = 2 * round;
-  if (chunk > 16384) chunk = 16384;  // its page table stays below 16 KB of LDS
-  return Plan{(int)chunk, (int)((tokens + chunk - 1) / chunk)};
+  int64_t tokens = a.max_len;  // live tokens of a sequence, from the tile that holds the first one
+  if (a.window > 0 && tokens > (int64_t)a.window + kTile) tokens = (int64_t)a.window + kTile;
+  const int64_t tiles = tokens <= kTile ? 1 : (tokens + kTile - 1) / kTile;
+  const int wide = 16 * row_tiles(a);
+  Plan p{};
+  p.rows = (int64_t)a.B * a.Hkv * ((a.Hq / a.Hkv + wide - 1) / wide);
+  const int64_t parts = (a.D <= 128 ? 8 : 4) * cus;  // waves that are resident together
+  if (tiles <= 4) {
+    p.per = (int)tiles;
+    p.splits = 1;
+  } else if (a.B == 1 || p.rows * tiles <= parts) {
+    p.per = (int)((p.rows * tiles + parts - 1) / parts);
+    p.splits = (int)((tiles + p.per - 1) / p.per);
+  }
+  if (p.per > 0) {
+    p.waves = (int)(p.rows * p.splits);
+    p.by_row = p.splits > 1;
+    return p;
+  }
+  while ((int64_t)2 << p.log2_parts <= parts) p.log2_parts++;
+  p.waves = 1 << p.log2_parts;
+  p.by_row = p.rows <= p.waves;
+  return p;
 }
 
 template <int D, bool FP8, int RT>
 hipError_t launch_decode(const DecodeArgs &a, const Plan &p, float *part, hipStream_t stream) {
-  constexpr int NW = kWaves;
-  const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT);
-  const size_t join = (size_t)NW / 2 * 16 * RT * (D + 6) * sizeof(float);
-  const size_t lines = (size_t)(p.chunk / 16) * sizeof(int64_t);
-  const size_t lds = join > lines ? join : lines;
-  auto *kernel = decode_kernel<D, FP8, RT, NW>;
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
+  Cut *cuts = reinterpret_cast<Cut *>(part + 2 * (size_t)p.waves * part_floats(D, RT));
+  hipLaunchKernelGGL((decode_kernel<D, FP8, RT>), dim3((unsigned)((p.waves + kWaves - 1) / kWaves)), dim3(kThreads), 0,
+                     stream, a, p, part, cuts);
+  if (p.per == 0 || p.splits > 1) {
+    const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
+    const dim3 grid((unsigned)(p.by_row ? p.rows : p.waves), (unsigned)(p.by_row || heads < 4 ? heads : 4));
+    if (p.rows * 64 <= p.waves)
+      hipLaunchKernelGGL((join_kernel<D, RT, 16>), grid, dim3(1024), 0, stream, a, p.log2_parts, (const float *)part,
+                         (const Cut *)cuts);
+    else
+      hipLaunchKernelGGL((join_kernel<D, RT, 4>), grid, dim3(256), 0, stream, a, p.log2_parts, (const float *)part,
+                         (const Cut *)cuts);
   }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)p.splits, (unsigned)(a.Hkv * bands), (unsigned)a.B), dim3(64 * NW), lds,
-                     stream, a, p.chunk, p.splits, part);
-  if (p.splits > 1)
-    hipLaunchKernelGGL(join_kernel<D>, dim3((unsigned)a.Hq, (unsigned)a.B), dim3(64), 0, stream, a, p.chunk, p.splits,
-                       (const float *)part);
   return hipGetLastError();
 }
 
 template <int D, bool FP8>
 hipError_t launch_rows(const DecodeArgs &a, const Plan &p, float *part, hipStream_t stream) {
-  if (a.Hq / a.Hkv <= 16) return launch_decode<D, FP8, 1>(a, p, part, stream);
-  return launch_decode<D, FP8, 2>(a, p, part, stream);
+  if constexpr (D < 256) {
+    if (row_tiles(a) == 2) return launch_decode<D, FP8, 2>(a, p, part, stream);
+  }
+  return launch_decode<D, FP8, 1>(a, p, part, stream);
 }
 
 template <int D>
@@ -503,7 +685,9 @@ hipError_t launch_dim(const DecodeArgs &a, const Plan &p, float *part, hipStream
 
 size_t paged_decode_partial_bytes(const DecodeArgs &a, int cus) {
   const Plan p = plan_decode(a, cus);
-  return p.splits > 1 ? (size_t)a.B * p.splits * partial_floats(a.Hq, a.D) * sizeof(float) : 0;
+  if (p.per > 0 && p.splits == 1) return 0;
+  return 2 * (size_t)p.waves * part_floats(a.D, row_tiles(a)) * sizeof(float) +
+         (size_t)(p.by_row ? p.rows : p.waves) * sizeof(Cut);
 }
 
 hipError_t launch_paged_decode(const DecodeArgs &a, float *part, hipStream_t stream) {
