@@ -40,6 +40,7 @@ MAX_LINEAR_M = 64  # the fused-quantization calls take decode-sized batches
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None
 
 
 class Fp8LinError(RuntimeError):
@@ -56,8 +57,8 @@ def load_library():
     with _lock:
         if _lib is not None:
             return _lib
-        if not os.path.exists(LIB_PATH):
-            raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
+        if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_HERE, "_marshal.so"))):
+            raise RuntimeError(f"{LIB_PATH} or _marshal.so beside it is missing: build it with __graft_entry__.build() "
                                "or python sparse_gemm_linears_amd/build.py")
         lib = ctypes.CDLL(LIB_PATH)
         P, I, F, B = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
@@ -411,32 +412,21 @@ def fp8_grouped_gemm(xq, xs, wq, ws, offsets: torch.Tensor, y: torch.Tensor | No
     return y
 
 
-def _same_device(first: torch.Tensor, *others):
-    """The library launches on the current device: every tensor has to be there."""
-    at = torch.cuda.current_device()
-    for t in (first, *others):
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"expected tensors on the current device (cuda:{at}), got one on {t.device}")
+# The decoder-layer calls: small ones are bound by the host, so their checks and
+# allocations are in _marshal.so (csrc/marshal.cpp), which makes the C call.
+
+def _marshal_module():
+    global _marshal
+    if _marshal is None:
+        load_library()
+        from . import _marshal as module
+        module.set_status_check(_check)
+        _marshal = module
+    return _marshal
 
 
-def _add_rmsnorm(fn, x, w, res, eps, keep_y, quantize, h, y, q, s, scale_dtype):
-    _want(x, "x", torch.bfloat16)
-    M, K = x.shape
-    _want(w, "w", torch.bfloat16, (K,))
-    if not keep_y and not quantize:
-        raise ValueError(f"{fn}: keep_y=False needs quantize=True")
-    if res is not None:
-        _want(res, "res", torch.bfloat16, (M, K))
-        h = _out(h, "h", (M, K), torch.bfloat16, x)
-    elif h is not None:
-        raise ValueError(f"{fn}: h is written only where res is given (without it h = x)")
-    y = _out(y, "y", (M, K), torch.bfloat16, x) if keep_y else None
-    q = _out(None if q is None else _codes(q), "q", (M, K), torch.uint8, x) if quantize else None
-    s = _out(s, "scales", (M, K // GROUP), scale_dtype, x) if quantize else None
-    _same_device(x, w, res, h, y, q, s)
-    _check(fn, getattr(load_library(), fn)(_ptr(x), _ptr(res), _ptr(w), eps, M, K, _ptr(h), _ptr(y), _ptr(q), _ptr(s),
-                                           _stream(x)))
-    return h, y, q, s
+def _stream_of(t):
+    return _stream(t) if isinstance(t, torch.Tensor) and t.is_cuda else 0
 
 
 def fp8_add_rmsnorm(x, w, res=None, eps: float = 1e-5, keep_y: bool = False, quantize: bool = True, h=None, y=None,
@@ -444,85 +434,28 @@ def fp8_add_rmsnorm(x, w, res=None, eps: float = 1e-5, keep_y: bool = False, qua
     """h = x + res (None without res), v = h / sqrt(mean(h^2) + eps) * w over rows of x [M,K] bf16, w [K] bf16.
     Returns (h [M,K] bf16, y = v [M,K] bf16 or None, q [M,K] e4m3 codes of v, s [M,K/128] fp32); ``h=res`` updates
     the residual stream in place; without ``quantize`` q and s are None."""
-    return _add_rmsnorm("fp8_add_rmsnorm", x, w, res, eps, keep_y, quantize, h, y, q, s, torch.float32)
+    return _marshal_module().add_rmsnorm(False, x, w, res, eps, keep_y, quantize, h, y, q, s, _stream_of(x))
 
 
 def fp8_add_rmsnorm_ue8m0(x, w, res=None, eps: float = 1e-5, keep_y: bool = False, quantize: bool = True, h=None,
                           y=None, q=None, e=None):
     """fp8_add_rmsnorm with UE8M0 scale bytes e [M,K/128]; returns (h, y, q, e)."""
-    return _add_rmsnorm("fp8_add_rmsnorm_ue8m0", x, w, res, eps, keep_y, quantize, h, y, q,
-                        None if e is None else _exps(e), torch.uint8)
-
-
-def _want_cache(k_cache, v_cache, k_scale, v_scale, fp8: bool):
-    dtype = torch.uint8 if fp8 else torch.bfloat16
-    _want(k_cache, "k_cache", dtype)
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache: expected [pages, heads, page_size, head_dim], got {tuple(k_cache.shape)}")
-    _want(v_cache, "v_cache", dtype, k_cache.shape)
-    if fp8:
-        _want(k_scale, "k_scale", torch.float32, k_cache.shape[:3])
-        _want(v_scale, "v_scale", torch.float32, k_cache.shape[:3])
-    return k_cache.shape
-
-
-def _kv_rope_append(fn, qkv, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale, interleaved, q, fp8):
-    pages, Hkv, page, D = _want_cache(k_cache, v_cache, k_scale, v_scale, fp8)
-    _want(qkv, "qkv", torch.bfloat16)
-    T, width = qkv.shape
-    Hq = width // D - 2 * Hkv
-    if Hq <= 0 or width % D:
-        raise ValueError(f"qkv: {width} columns do not hold query heads beside 2 x {Hkv} heads of {D}")
-    _want(positions, "positions", torch.int32, (T,))
-    _want(slots, "slots", torch.int64, (T,))
-    _want(cos_sin, "cos_sin", torch.float32)
-    max_pos, rot = cos_sin.shape
-    q = _out(q, "q", (T, Hq, D), torch.bfloat16, qkv)
-    _same_device(qkv, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale, q)
-    scales = (_ptr(k_scale), _ptr(v_scale)) if fp8 else ()
-    _check(fn, getattr(load_library(), fn)(
-        _ptr(qkv), _ptr(positions), _ptr(slots), _ptr(cos_sin), T, Hq, Hkv, D, rot, int(interleaved), max_pos, pages,
-        page, _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _stream(qkv)))
-    return q
+    return _marshal_module().add_rmsnorm(True, x, w, res, eps, keep_y, quantize, h, y, q, e, _stream_of(x))
 
 
 def kv_rope_append(qkv, positions, slots, cos_sin, k_cache, v_cache, interleaved: bool = False, q=None):
     """Rotate the query and key heads of qkv [T,(Hq+2Hkv)D] bf16 by row positions[t] of cos_sin [max_pos,rot] fp32
     and write keys and values to cache line slots[t] (int64; negative: not stored) of k_cache and v_cache
     [pages,Hkv,page,D] bf16.  Returns the rotated queries [T,Hq,D] bf16."""
-    return _kv_rope_append("kv_rope_append", qkv, positions, slots, cos_sin, k_cache, v_cache, None, None, interleaved,
-                           q, False)
+    return _marshal_module().rope_append(False, qkv, positions, slots, cos_sin, k_cache, v_cache, None, None,
+                                         interleaved, q, _stream_of(qkv))
 
 
 def kv_rope_append_fp8(qkv, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale, interleaved: bool = False,
                        q=None):
     """kv_rope_append into an e4m3 cache: codes [pages,Hkv,page,D] and fp32 scales [pages,Hkv,page]."""
-    return _kv_rope_append("kv_rope_append_fp8", qkv, positions, slots, cos_sin, _codes(k_cache), _codes(v_cache),
-                           k_scale, v_scale, interleaved, q, True)
-
-
-def _paged_decode(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale, softcap, window, max_len,
-                  return_lse, o, lse, fp8):
-    pages, Hkv, page, D = _want_cache(k_cache, v_cache, k_scale, v_scale, fp8)
-    _want(q, "q", torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q: expected [batch, heads, {D}], got {tuple(q.shape)}")
-    B, Hq, _ = q.shape
-    _want(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected [{B}, pages], got {tuple(block_table.shape)}")
-    _want(seq_lens, "seq_lens", torch.int32, (B,))
-    max_pages = block_table.shape[1]
-    o = _out(o, "o", (B, Hq, D), torch.bfloat16, q)
-    if return_lse or lse is not None:
-        lse = _out(lse, "lse", (B, Hq), torch.float32, q)
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse)
-    scales = (_ptr(k_scale), _ptr(v_scale)) if fp8 else ()
-    _check(fn, getattr(load_library(), fn)(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_table), _ptr(seq_lens), B, Hq, Hkv, D, pages, page,
-        max_pages, max_pages * page if max_len is None else max_len, D ** -0.5 if scale is None else scale, softcap,
-        window, _ptr(o), _ptr(lse), _stream(q)))
-    return (o, lse) if return_lse else o
+    return _marshal_module().rope_append(True, qkv, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale,
+                                         interleaved, q, _stream_of(qkv))
 
 
 def paged_decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0,
@@ -531,13 +464,13 @@ def paged_decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=Non
     pages block_table[b] (int32) of k_cache and v_cache [pages,Hkv,page,D] bf16.  scale: D^-0.5 by default; softcap >
     0 caps the scores; window > 0 keeps the last `window` tokens; max_len: a bound on seq_lens known to the host (the
     table's width by default; longer sequences are cut to it).  Returns o [B,Hq,D] bf16, or (o, lse [B,Hq] fp32)."""
-    return _paged_decode("paged_decode_attention", q, k_cache, v_cache, None, None, block_table, seq_lens, scale,
-                         softcap, window, max_len, return_lse, o, lse, False)
+    return _marshal_module().paged_decode(False, q, k_cache, v_cache, None, None, block_table, seq_lens, scale, softcap,
+                                          window, max_len, return_lse, o, lse, _stream_of(q))
 
 
 def paged_decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale=None,
                                softcap: float = 0.0, window: int = 0, max_len=None, return_lse: bool = False, o=None,
                                lse=None):
     """paged_decode_attention over an e4m3 cache: codes [pages,Hkv,page,D] and fp32 scales [pages,Hkv,page]."""
-    return _paged_decode("paged_decode_attention_fp8", q, _codes(k_cache), _codes(v_cache), k_scale, v_scale,
-                         block_table, seq_lens, scale, softcap, window, max_len, return_lse, o, lse, True)
+    return _marshal_module().paged_decode(True, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
+                                          softcap, window, max_len, return_lse, o, lse, _stream_of(q))
