@@ -15,13 +15,13 @@
 // A row is one key head of one sequence with up to 16 RT of its query heads, and
 // work is counted in tiles of 32 tokens.  Lengths are known on the device only,
 // and a grid made for the longest sequence leaves most of it without work in a
-// ragged batch.  So a fixed number of waves divides all tiles of the batch into
-// even shares: each finds its share from the lengths and takes the rows in it in
-// turn, the next tile always loading while one is used.  Waves work alone: no
-// barrier, no LDS.  A wave leaves a partial for the row that its share begins
-// inside and for the one that it ends inside; join_kernel adds the partials of a
-// row in order.  One sequence alone, and batches that give each wave a tile at
-// most, are divided by the grid, without the search.
+// ragged batch.  So a fixed number of waves divides the batch into even shares:
+// each finds its share from the lengths and takes the rows in it in turn, alone,
+// without barriers; twelve waves on a compute unit keep its loads going.  A wave
+// leaves a partial for the row that its share begins inside and for the one that it
+// ends inside, and join_kernel adds the partials of a row in order.  One sequence
+// alone, and batches that give each wave a tile at most, are divided by the grid,
+// without the search.  Rows of short sequences have a workgroup each (row_kernel).
 //
 // Layouts (v_mfma_f32_16x16x32_bf16: lane l, n = l % 16, g = l / 16):
 //   scores   A = K: row n is token n of a half tile, B = Q: column n is a query
@@ -277,9 +277,14 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int len) {
 
 // How work is divided.  per == 0: even shares; the rows of a sequence follow
 // each other (bands of query heads within a key head), and wave i of
-// 2^log2_parts takes tiles share_start(i) .. share_start(i + 1) - 1 of all.
+// 2^log2_parts takes units share_start(i) .. share_start(i + 1) - 1 of all.  A
+// unit is a tile, and one more for the end of each row, which costs about as much
+// (shares of equal tiles took 77 us on 64 sequences of 1 to 8192 tokens where
+// sequences of equal length took 63).
 // per > 0: each row has `splits` waves of `per` tiles.
+// row_waves > 0: each row has one workgroup of that many waves (row_kernel).
 struct Plan {
+  int row_waves;
   int per, splits, log2_parts;
   int waves;
   int64_t rows;  // of the batch
@@ -304,18 +309,19 @@ struct Cut {
 // wave has two slots.
 __host__ __device__ constexpr size_t part_floats(int D, int RT) { return (size_t)16 * RT * (D + 2); }
 
-// A tile of the batch: the tile `tile` of row `band` of sequence b.
+// A unit of the batch: tile `tile` of row `band` of sequence b, or (tile ==
+// tiles_of) the row's end.
 struct Place {
   int b, band, tile, len;
 };
 
-// All tiles of the batch; before and upto: those of the sequences before this
+// All units of the batch; before and upto: those of the sequences before this
 // lane's run of sequences, and with it.
-__device__ __forceinline__ int64_t batch_tiles(const DecodeArgs &a, int rows, int lane, int64_t &before,
+__device__ __forceinline__ int64_t batch_units(const DecodeArgs &a, int rows, int lane, int64_t &before,
                                                int64_t &upto) {
   const int per = (a.B + 63) / 64, b0 = lane * per, b1 = min(a.B, b0 + per);
   int64_t mine = 0;
-  for (int i = b0; i < b1; i++) mine += tiles_of(a, length_of(a, i));
+  for (int i = b0; i < b1; i++) mine += tiles_of(a, length_of(a, i)) + 1;
   mine *= rows;
   upto = mine;
 #pragma unroll
@@ -327,18 +333,64 @@ __device__ __forceinline__ int64_t batch_tiles(const DecodeArgs &a, int rows, in
   return __shfl(upto, 63, 64);
 }
 
+// A row: key head kvh of sequence b with `heads` query heads from q0 of all on.
+struct Row {
+  int kvh, heads;
+  int64_t q0;
+  __device__ Row(const DecodeArgs &a, int b, int band, int RT) {
+    const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT);
+    kvh = band / bands;
+    const int head0 = (band - kvh * bands) * 16 * RT;
+    heads = min(group - head0, 16 * RT);
+    q0 = (int64_t)b * a.Hq + kvh * group + head0;
+  }
+};
+
+template <int D, bool FP8, int RT>
+__device__ __forceinline__ void load_queries(v8bf (&qf)[RT][D / 32], const DecodeArgs &a, const Row &row, int n,
+                                             int g) {
+#pragma unroll
+  for (int r = 0; r < RT; r++) {
+#pragma unroll
+    for (int c = 0; c < D / 32; c++) {
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      if (16 * r + n < row.heads)
+        raw = *reinterpret_cast<const uint4 *>(a.q + (row.q0 + 16 * r + n) * D + 64 * (c >> 1) + 16 * g + 8 * (c & 1));
+      qf[r][c] = as_bf16x8(raw.x, raw.y, raw.z, raw.w);
+    }
+  }
+}
+
+template <int D, int RT>
+__device__ __forceinline__ void clear_state(State<D> (&st)[RT]) {
+#pragma unroll
+  for (int r = 0; r < RT; r++) {
+    st[r].m = -INFINITY;
+    st[r].l = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) st[r].o[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// The cache line of `token` of sequence b (which must be below max_len).
+__device__ __forceinline__ int64_t line_of(const DecodeArgs &a, int b, int kvh, int token) {
+  const int p = (int)((uint32_t)token / (uint32_t)a.page_size);
+  const int page = min(max(a.block_table[(int64_t)b * a.max_pages + p], 0), a.pages - 1);
+  return ((int64_t)page * a.Hkv + kvh) * a.page_size + (token - p * a.page_size);
+}
+
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int from_lane(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
 __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
   return (int64_t)(uint32_t)from_lane((int)x, lane) | (int64_t)from_lane((int)(x >> 32), lane) << 32;
 }
 
-// Quotient of a tile's place among a sequence's tiles by the tiles of a row.
-__device__ __forceinline__ int row_of(int64_t inside, int tiles) {
-  return inside >> 31 ? (int)(inside / tiles) : (int)((uint32_t)inside / (uint32_t)tiles);
+// Quotient of a unit's place among a sequence's units by the units of a row.
+__device__ __forceinline__ int row_of(int64_t inside, int units) {
+  return inside >> 31 ? (int)(inside / units) : (int)((uint32_t)inside / (uint32_t)units);
 }
 
-__device__ __forceinline__ Place find_tile(const DecodeArgs &a, int rows, int lane, int64_t at, int64_t before,
+__device__ __forceinline__ Place find_unit(const DecodeArgs &a, int rows, int lane, int64_t at, int64_t before,
                                            int64_t upto) {
   const int per = (a.B + 63) / 64, b0 = lane * per, b1 = min(a.B, b0 + per);
   int b = 0, band = 0, tile = 0, len = 0;
@@ -347,10 +399,10 @@ __device__ __forceinline__ Place find_tile(const DecodeArgs &a, int rows, int la
     b = b0;
     len = length_of(a, b);
     int64_t inside = at - before;
-    for (int64_t n; b + 1 < b1 && inside >= (n = (int64_t)tiles_of(a, len) * rows); inside -= n) len = length_of(a, ++b);
-    const int tiles = tiles_of(a, len);
-    band = row_of(inside, tiles);
-    tile = (int)(inside - (int64_t)band * tiles);
+    for (int64_t n; b + 1 < b1 && inside >= (n = (int64_t)(tiles_of(a, len) + 1) * rows); inside -= n) len = length_of(a, ++b);
+    const int units = tiles_of(a, len) + 1;
+    band = row_of(inside, units);
+    tile = (int)(inside - (int64_t)band * units);
   }
   const int src = __ffsll((unsigned long long)__ballot(mine)) - 1;
   return Place{from_lane(b, src), from_lane(band, src), from_lane(tile, src), from_lane(len, src)};
@@ -365,8 +417,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
   const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT), rows = a.Hkv * bands;
 
   Place at;      // the next tile to list
-  int64_t left;  // tiles of the share that are not listed yet
-  int64_t total = 0, position = 0;  // tiles of the batch, and where the share starts in them
+  int64_t left;  // units of the share that are not listed yet
+  int64_t total = 0, position = 0;  // units of the batch, and where the share starts in them
   if (plan.per > 0) {
     const int row = self / plan.splits, split = self - row * plan.splits;
     at.b = row / rows;
@@ -377,54 +429,42 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
     if (left <= 0) return;
   } else {
     int64_t before, upto;
-    total = batch_tiles(a, rows, lane, before, upto);
+    total = batch_units(a, rows, lane, before, upto);
     position = share_start(self, total, plan.log2_parts);
     left = share_start(self + 1, total, plan.log2_parts) - position;
     if (!plan.by_row && lane == 0) cuts[self].slot = -1;
-    if (left <= 0) return;  // there are more waves than tiles
-    at = find_tile(a, rows, lane, position, before, upto);
+    if (left <= 0) return;  // there are more waves than units
+    at = find_unit(a, rows, lane, position, before, upto);
+  }
+  auto next_row = [&] {
+    at.tile = 0;
+    if (++at.band == rows) {
+      at.band = 0;
+      at.b++;
+      at.len = uniform(length_of(a, at.b));
+    }
+  };
+  if (at.tile == tiles_of(a, at.len)) {  // a row's end alone: nothing is left to do for it
+    if (--left == 0) return;
+    position++;
+    next_row();
   }
   bool started = true;        // whether this is the share's first row
   int row_begin = at.tile;    // first tile of the present row that is in the share
   int64_t row_position = position - at.tile;  // of the present row's first tile
 
   v8bf qf[RT][D / 32];
-  auto load_q = [&](int b, int band) {
-    const int kvh = band / bands, head0 = (band - kvh * bands) * 16 * RT;
-    const int heads = min(group - head0, 16 * RT);
-    const uint16_t *src = a.q + ((int64_t)b * a.Hq + kvh * group + head0) * D;
-#pragma unroll
-    for (int r = 0; r < RT; r++) {
-#pragma unroll
-      for (int c = 0; c < D / 32; c++) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (16 * r + n < heads)
-          raw = *reinterpret_cast<const uint4 *>(src + (16 * r + n) * D + 64 * (c >> 1) + 16 * g + 8 * (c & 1));
-        qf[r][c] = as_bf16x8(raw.x, raw.y, raw.z, raw.w);
-      }
-    }
-  };
-  load_q(at.b, at.band);
   State<D> st[RT];
-  auto clear = [&] {
-#pragma unroll
-    for (int r = 0; r < RT; r++) {
-      st[r].m = -INFINITY;
-      st[r].l = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; i++) st[r].o[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
-  };
-  clear();
+  bool fresh = true;  // whether the next tile begins a row (here)
 
   while (left > 0) {
-    // list the next tiles: lane x finds tile x and its cache lines
+    // list the next units: lane x finds unit x and its cache lines
     const int count = (int)min(left, (int64_t)kListed);
     int rb = at.b, rband = at.band, rtile = at.tile + lane, rlen = at.len;
-    if (count > tiles_of(a, at.len) - at.tile) {  // they reach past the present row
-      const int len = length_of(a, at.b + lane), tiles = tiles_of(a, len);
-      // tiles of sequence at.b + lane from here on (more than 1024 are as good), and their running sum
-      const int64_t all = (int64_t)tiles * rows - (lane == 0 ? (int64_t)at.band * tiles + at.tile : 0);
+    if (count > tiles_of(a, at.len) + 1 - at.tile) {  // they reach past the present row
+      const int len = length_of(a, at.b + lane), units = tiles_of(a, len) + 1;
+      // units of sequence at.b + lane from here on (more than 1024 are as good), and their running sum
+      const int64_t all = (int64_t)units * rows - (lane == 0 ? (int64_t)at.band * units + at.tile : 0);
       int mine = at.b + lane < a.B ? (int)min(all, (int64_t)1024) : 0, upto = mine;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -436,12 +476,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
       for (int step = 32; step; step >>= 1)
         if (__shfl(upto, s + step - 1, 64) <= lane) s += step;
       const int before = __shfl(upto - mine, s, 64);
-      const int stiles = __shfl(tiles, s, 64);
+      const int sunits = __shfl(units, s, 64);
       rlen = __shfl(len, s, 64);
       rb = at.b + s;
-      const int64_t inside = lane - before + (s == 0 ? (int64_t)at.band * stiles + at.tile : 0);
-      rband = row_of(inside, stiles);
-      rtile = (int)(inside - (int64_t)rband * stiles);
+      const int64_t inside = lane - before + (s == 0 ? (int64_t)at.band * sunits + at.tile : 0);
+      rband = row_of(inside, sunits);
+      rtile = (int)(inside - (int64_t)rband * sunits);
     }
     const int rtoken = first_token(rlen, a.window) + rtile * kTile;
     int64_t rline[2] = {0, 0};  // of tokens past the end, which count for nothing: any line will do
@@ -449,55 +489,45 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
 #pragma unroll
     for (int hh = 0; hh < 2; hh++) {
       const int token = rtoken + 16 * hh;
-      if (lane < count && token < rlen) {
-        const int p = (int)((uint32_t)token / (uint32_t)a.page_size);
-        const int page = min(max(a.block_table[(int64_t)rb * a.max_pages + p], 0), a.pages - 1);
-        rline[hh] = ((int64_t)page * a.Hkv + rkvh) * a.page_size + (token - p * a.page_size);
-      }
+      if (lane < count && token < rlen) rline[hh] = line_of(a, rb, rkvh, token);
     }
-    // where the next list begins: one tile after the last of this one
+    // where the next list begins: one unit after the last of this one
     at = Place{from_lane(rb, count - 1), from_lane(rband, count - 1), from_lane(rtile, count - 1) + 1,
                from_lane(rlen, count - 1)};
     left -= count;
-    if (left > 0 && at.tile == tiles_of(a, at.len)) {
-      at.tile = 0;
-      if (++at.band == rows) {
-        at.band = 0;
-        at.b++;
-        at.len = uniform(length_of(a, at.b));
-      }
-    }
+    if (left > 0 && at.tile > tiles_of(a, at.len)) next_row();
     auto load = [&](Tile<D, FP8> &t, int i) {
       const int64_t line[2] = {from_lane(rline[0], i), from_lane(rline[1], i)};
       load_tile<D, FP8>(t, a, line, n, g);
     };
     for (int i = 0; i < count; i++) {
-      const int token = from_lane(rtoken, i), len = from_lane(rlen, i);
+      const int token = from_lane(rtoken, i), len = from_lane(rlen, i), tiles = tiles_of(a, len);
+      if (from_lane(rtile, i) == tiles) continue;  // a row's end
+      if (fresh) {
+        load_queries<D, FP8, RT>(qf, a, Row(a, from_lane(rb, i), from_lane(rband, i), RT), n, g);
+        clear_state(st);
+        fresh = false;
+      }
       Tile<D, FP8> now;
       load(now, i);
       use_tile<D, FP8, RT>(now, a, qf, st, token, a.window > 0 ? max(0, len - a.window) : 0, len, g);
       const bool row_ends = token + kTile >= len, share_ends = i + 1 == count && left == 0;
       if (row_ends || share_ends) {
         const int b = from_lane(rb, i), band = from_lane(rband, i);
-        if (!share_ends)  // the next row's queries
-          load_q(i + 1 < count ? from_lane(rb, (i + 1) & 63) : at.b, i + 1 < count ? from_lane(rband, (i + 1) & 63) : at.band);
-        const int tiles = tiles_of(a, len);
         const bool whole = row_begin == 0 && row_ends;
         const int slot = 2 * self + (started ? 0 : 1);
-        const int kvh = band / bands, head0 = (band - kvh * bands) * 16 * RT;
-        const int heads = min(group - head0, 16 * RT);
-        const int64_t q0 = (int64_t)b * a.Hq + kvh * group + head0;
+        const Row row(a, b, band, RT);
 #pragma unroll
         for (int r = 0; r < RT; r++) {
           const int head = 16 * r + n;
           float l = st[r].l;
           l += __shfl_xor(l, 16, 64);
           l += __shfl_xor(l, 32, 64);
-          if (head >= heads) continue;
+          if (head >= row.heads) continue;
           // this lane holds values D / 4 g .. + D / 4 - 1 of its head
           if (whole) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t *dst = a.o + (q0 + head) * D + D / 4 * g;
+            uint16_t *dst = a.o + (row.q0 + head) * D + D / 4 * g;
 #pragma unroll
             for (int e = 0; e < D / 4; e += 8) {
               float v[8];
@@ -505,7 +535,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
               for (int k = 0; k < 8; k++) v[k] = st[r].o[(e + k) % (D / 16)][(e + k) / (D / 16)] * inv;
               *reinterpret_cast<uint4 *>(dst + e) = pack8(v);
             }
-            if (a.lse && g == 0) a.lse[q0 + head] = l == 0.f ? -INFINITY : kLn2 * (st[r].m + log2f(l));
+            if (a.lse && g == 0) a.lse[row.q0 + head] = l == 0.f ? -INFINITY : kLn2 * (st[r].m + log2f(l));
           } else {
             float *base = part + slot * part_floats(D, RT), *dst = base + head * D + D / 4 * g;
 #pragma unroll
@@ -526,30 +556,103 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
           cuts[plan.by_row ? (int64_t)b * rows + band : (int64_t)self] =
               Cut{total, row_position + tiles, b, band, whole ? -1 : slot, parts, self, 0};
         }
-        clear();
+        fresh = true;
         started = false;
         row_begin = 0;
-        row_position += tiles;
+        row_position += tiles + 1;
       }
     }
   }
 }
 
-// Joins the parts of a divided row, in a fixed order: workgroup (i, y) takes row
-// i of the list, and of its query heads y, y + gridDim.y, ...  Wave w adds parts
-// w, w + JW, ... with a running maximum (eight loads in flight), then the waves'
-// sums are added.  A part weighs 2^(m - top).
-template <int D, int RT, int JW>
-__global__ __launch_bounds__(64 * JW) void join_kernel(DecodeArgs a, int log2_parts, const float *part,
-                                                       const Cut *cuts) {
+// One row a workgroup, for short sequences: wave w takes tiles w, w + WAVES, ...
+// and the waves' states are added through LDS, in a fixed order.
+template <int D, bool FP8, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void row_kernel(DecodeArgs a) {
+  constexpr int kPad = D + 4;  // a head in LDS, off the bank period
+  extern __shared__ __align__(16) float box[];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  const int group = a.Hq / a.Hkv, rows = a.Hkv * ((group + 16 * RT - 1) / (16 * RT));
+  const int b = (int)blockIdx.x / rows;
+  const Row row(a, b, (int)blockIdx.x - b * rows, RT);
+  float *box_m = box, *box_l = box_m + WAVES * row.heads, *box_o = box_l + WAVES * row.heads;  // 32 heads bytes apart
+  v8bf qf[RT][D / 32];
+  load_queries<D, FP8, RT>(qf, a, row, n, g);
+  // lane x looks up the half tiles of the wave's tile x; without a window before the length is known
+  const int mine = kTile * (wave + WAVES * (lane >> 1)) + 16 * (lane & 1);
+  int64_t early = 0;
+  if (a.window == 0 && mine < a.max_len) early = line_of(a, b, row.kvh, mine);
+  const int len = uniform(length_of(a, b)), first = first_token(len, a.window), tiles = tiles_of(a, len);
+  if (a.window > 0 && first + mine < len) early = line_of(a, b, row.kvh, first + mine);
+  State<D> st[RT];
+  clear_state(st);
+  for (int i = wave, x = 0; i < tiles && len > 0; i += WAVES, x++) {
+    const int token = first + kTile * i;
+    // a half tile past the end counts for nothing: any line will do
+    const int64_t line[2] = {from_lane(early, 2 * x), token + 16 < len ? from_lane(early, 2 * x + 1) : 0};
+    Tile<D, FP8> t;
+    load_tile<D, FP8>(t, a, line, n, g);
+    use_tile<D, FP8, RT>(t, a, qf, st, token, a.window > 0 ? max(0, len - a.window) : 0, len, g);
+  }
+#pragma unroll
+  for (int r = 0; r < RT; r++) {
+    const int head = 16 * r + n;
+    float l = st[r].l;
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (head >= row.heads) continue;
+    float *dst = box_o + (wave * row.heads + head) * kPad + D / 4 * g;
+#pragma unroll
+    for (int e = 0; e < D / 4; e += 4) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) v[k] = st[r].o[(e + k) % (D / 16)][(e + k) / (D / 16)];
+      *reinterpret_cast<float4 *>(dst + e) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    if (g == 0) {
+      box_m[wave * row.heads + head] = st[r].m;
+      box_l[wave * row.heads + head] = l;
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < row.heads * (D / 4); c += 64 * WAVES) {
+    const int head = c / (D / 4), d = c % (D / 4) * 4;
+    float top = -INFINITY, l = 0.f, o[4] = {};
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) top = fmaxf(top, box_m[w * row.heads + head]);
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) {
+      const float m = box_m[w * row.heads + head], f = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
+      const float4 x = *reinterpret_cast<const float4 *>(box_o + (w * row.heads + head) * kPad + d);
+      l += box_l[w * row.heads + head] * f;
+      o[0] += x.x * f;
+      o[1] += x.y * f;
+      o[2] += x.z * f;
+      o[3] += x.w * f;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(a.o + (row.q0 + head) * D + d) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (a.lse && d == 0) a.lse[row.q0 + head] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+  }
+}
+
+// Joins the parts of divided rows, in a fixed order.  Workgroup (i, y) takes row i
+// of the list and HEADS of its query heads.  Where the row has few parts each wave
+// joins one head alone, else all waves share the parts of one head after the
+// other, through LDS.  Eight parts are in flight at a time, under a running
+// maximum; a part weighs 2^(m - top).
+template <int D, int RT, int WAVES, int HEADS>
+__global__ __launch_bounds__(64 * WAVES) void join_kernel(DecodeArgs a, int log2_parts, const float *part,
+                                                          const Cut *cuts) {
   constexpr int E = D / 64;
-  __shared__ float wave_top[JW], wave_l[JW], wave_o[JW][D];
+  __shared__ float wave_top[WAVES], wave_l[WAVES], wave_o[WAVES][D];
   const Cut cut = cuts[blockIdx.x];
   if (cut.slot < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT);
-  const int kvh = cut.band / bands, head0 = (cut.band - kvh * bands) * 16 * RT;
-  const int heads = min(group - head0, 16 * RT);
+  const int kvh = cut.band / bands, band_head = (cut.band - kvh * bands) * 16 * RT;
+  const int heads = min(group - band_head, 16 * RT);
   int parts = cut.parts;
   if (parts == 0) {
     // shares from the owner's on that start before the row's end
@@ -563,15 +666,17 @@ __global__ __launch_bounds__(64 * JW) void join_kernel(DecodeArgs a, int log2_pa
     }
     parts = low;
   }
-  for (int head = blockIdx.y; head < heads; head += gridDim.y) {
+  const bool alone = HEADS > 1 && parts <= 24;
+  const int step = alone ? 1 : WAVES, head_end = min(heads, (int)(blockIdx.y + 1) * HEADS);
+  for (int head = blockIdx.y * HEADS + (alone ? wave : 0); head < head_end; head += alone ? WAVES : 1) {
     float top = -INFINITY, l = 0.f, o[E] = {};
-    for (int k0 = wave; k0 < parts; k0 += 8 * JW) {
+    for (int k0 = alone ? 0 : wave; k0 < parts; k0 += 8 * step) {
       float m[8], lp[8], op[8][E];
 #pragma unroll
       for (int u = 0; u < 8; u++) {
-        const int k = min(k0 + JW * u, parts - 1);
+        const int k = min(k0 + step * u, parts - 1);
         const float *p = part + (size_t)(k == 0 ? cut.slot : 2 * (cut.owner + k)) * part_floats(D, RT);
-        m[u] = k0 + JW * u < parts ? p[16 * RT * D + head] : -INFINITY;
+        m[u] = p[16 * RT * D + head];
         lp[u] = p[16 * RT * (D + 1) + head];
 #pragma unroll
         for (int e = 0; e < E; e++) op[u][e] = p[head * D + E * lane + e];
@@ -586,13 +691,21 @@ __global__ __launch_bounds__(64 * JW) void join_kernel(DecodeArgs a, int log2_pa
       for (int e = 0; e < E; e++) o[e] *= shrink;
 #pragma unroll
       for (int u = 0; u < 8; u++) {
-        if (k0 + JW * u < parts) {
+        if (k0 + step * u < parts) {
           const float f = m[u] == top ? 1.f : __builtin_amdgcn_exp2f(m[u] - top);
           l += lp[u] * f;
 #pragma unroll
           for (int e = 0; e < E; e++) o[e] += op[u][e] * f;
         }
       }
+    }
+    const int64_t at = (int64_t)cut.b * a.Hq + kvh * group + band_head + head;
+    if (alone) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int e = 0; e < E; e++) a.o[at * D + E * lane + e] = (uint16_t)f32_to_bf16_rne(o[e] * inv);
+      if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+      continue;
     }
     __syncthreads();  // the boxes are free
     if (lane == 0) {
@@ -602,13 +715,12 @@ __global__ __launch_bounds__(64 * JW) void join_kernel(DecodeArgs a, int log2_pa
 #pragma unroll
     for (int e = 0; e < E; e++) wave_o[wave][E * lane + e] = o[e];
     __syncthreads();
-    const int64_t at = (int64_t)cut.b * a.Hq + kvh * group + head0 + head;
-    for (int d = threadIdx.x; d < D; d += 64 * JW) {
+    for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
       float high = -INFINITY, sum = 0.f, weight = 0.f;
 #pragma unroll
-      for (int w = 0; w < JW; w++) high = fmaxf(high, wave_top[w]);
+      for (int w = 0; w < WAVES; w++) high = fmaxf(high, wave_top[w]);
 #pragma unroll
-      for (int w = 0; w < JW; w++) {
+      for (int w = 0; w < WAVES; w++) {
         const float f = wave_top[w] == high ? 1.f : __builtin_amdgcn_exp2f(wave_top[w] - high);
         weight += wave_l[w] * f;
         sum += wave_o[w][d] * f;
@@ -631,11 +743,22 @@ Plan plan_decode(const DecodeArgs &a, int cus) {
   const int wide = 16 * row_tiles(a);
   Plan p{};
   p.rows = (int64_t)a.B * a.Hkv * ((a.Hq / a.Hkv + wide - 1) / wide);
-  const int64_t parts = (a.D <= 128 ? 8 : 4) * cus;  // waves that are resident together
-  if (tiles <= 4) {
-    p.per = (int)tiles;
-    p.splits = 1;
-  } else if (a.B == 1 || p.rows * tiles <= parts) {
+  // Short sequences: a workgroup for each row and no second kernel.  Measured
+  // (GPU time, 32 query and 8 key heads of 128, bf16) against the divided forms:
+  // one sequence of 300 tokens 7.1 us against 8.6, 16 of up to 500 9.3 / 12.4, 128
+  // of up to 500 23.2 / 27.7; with 25 tiles 10.7 / 8.9 for one sequence (one
+  // compute unit's loads bound it), with 32 16.7 / 21.1 for 32 sequences.
+  if (tiles <= (p.rows < 64 ? 16 : 32)) {
+    p.row_waves = a.D <= 128 && wide == 16 && p.rows <= cus ? 8 : 4;
+    return p;
+  }
+  // Waves that are resident together; fewer where a wave's tiles would be few
+  // beside the partials that it leaves (32 query heads on one key head of 128, 16
+  // sequences of 4000 to 8000 tokens: 2048 waves 36 us, 1024 27 us).
+  const int heads = a.Hq / a.Hkv < wide ? a.Hq / a.Hkv : wide;
+  const int64_t resident = (a.D <= 128 ? 8 : 4) * cus, fed = p.rows * tiles * 8 / heads;
+  const int64_t parts = resident < fed ? resident : fed > 512 ? fed : 512;
+  if (a.B == 1 || p.rows * tiles <= parts) {
     p.per = (int)((p.rows * tiles + parts - 1) / parts);
     p.splits = (int)((tiles + p.per - 1) / p.per);
   }
@@ -644,26 +767,49 @@ Plan plan_decode(const DecodeArgs &a, int cus) {
     p.by_row = p.splits > 1;
     return p;
   }
-  while ((int64_t)2 << p.log2_parts <= parts) p.log2_parts++;
+  while ((int64_t)3 << p.log2_parts <= 2 * parts) p.log2_parts++;  // the nearest power of two
   p.waves = 1 << p.log2_parts;
   p.by_row = p.rows <= p.waves;
   return p;
 }
 
+template <int D, bool FP8, int RT, int WAVES>
+hipError_t launch_row(const DecodeArgs &a, const Plan &p, hipStream_t stream) {
+  const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
+  const size_t lds = (size_t)WAVES * heads * (D + 6) * sizeof(float);
+  auto *kernel = row_kernel<D, FP8, RT, WAVES>;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3((unsigned)p.rows), dim3(64 * WAVES), lds, stream, a);
+  return hipGetLastError();
+}
+
 template <int D, bool FP8, int RT>
 hipError_t launch_decode(const DecodeArgs &a, const Plan &p, float *part, hipStream_t stream) {
+  if constexpr (D <= 128 && RT == 1) {
+    if (p.row_waves == 8) return launch_row<D, FP8, RT, 8>(a, p, stream);
+  }
+  if (p.row_waves) return launch_row<D, FP8, RT, 4>(a, p, stream);
   Cut *cuts = reinterpret_cast<Cut *>(part + 2 * (size_t)p.waves * part_floats(D, RT));
   hipLaunchKernelGGL((decode_kernel<D, FP8, RT>), dim3((unsigned)((p.waves + kWaves - 1) / kWaves)), dim3(kThreads), 0,
                      stream, a, p, part, cuts);
   if (p.per == 0 || p.splits > 1) {
     const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
-    const dim3 grid((unsigned)(p.by_row ? p.rows : p.waves), (unsigned)(p.by_row || heads < 4 ? heads : 4));
-    if (p.rows * 64 <= p.waves)
-      hipLaunchKernelGGL((join_kernel<D, RT, 16>), grid, dim3(1024), 0, stream, a, p.log2_parts, (const float *)part,
-                         (const Cut *)cuts);
+    const unsigned listed = (unsigned)(p.by_row ? p.rows : p.waves);
+    // many (row, head) pairs: four heads a workgroup (2048 pairs of 5 parts: 8.1 us with a workgroup for each, 5.1
+    // so); few: one, with more waves where a row has many parts (32 pairs of 25 parts: 8.3 us with four, 3.6 so)
+    if (p.rows * heads > 1024)
+      hipLaunchKernelGGL((join_kernel<D, RT, 4, 4>), dim3(listed, (unsigned)((heads + 3) / 4)), dim3(256), 0, stream, a,
+                         p.log2_parts, (const float *)part, (const Cut *)cuts);
+    else if (p.rows * 64 > p.waves)
+      hipLaunchKernelGGL((join_kernel<D, RT, 4, 1>), dim3(listed, (unsigned)heads), dim3(256), 0, stream, a,
+                         p.log2_parts, (const float *)part, (const Cut *)cuts);
     else
-      hipLaunchKernelGGL((join_kernel<D, RT, 4>), grid, dim3(256), 0, stream, a, p.log2_parts, (const float *)part,
-                         (const Cut *)cuts);
+      hipLaunchKernelGGL((join_kernel<D, RT, 16, 1>), dim3(listed, (unsigned)heads), dim3(1024), 0, stream, a,
+                         p.log2_parts, (const float *)part, (const Cut *)cuts);
   }
   return hipGetLastError();
 }
@@ -685,7 +831,7 @@ hipError_t launch_dim(const DecodeArgs &a, const Plan &p, float *part, hipStream
 
 size_t paged_decode_partial_bytes(const DecodeArgs &a, int cus) {
   const Plan p = plan_decode(a, cus);
-  if (p.per > 0 && p.splits == 1) return 0;
+  if (p.row_waves || (p.per > 0 && p.splits == 1)) return 0;
   return 2 * (size_t)p.waves * part_floats(a.D, row_tiles(a)) * sizeof(float) +
          (size_t)(p.by_row ? p.rows : p.waves) * sizeof(Cut);
 }
