@@ -6,6 +6,7 @@
 // amax / 448 for each token and head.  HBM-bound for many tokens (each value
 // is read once and written once), two memory latencies and the launch for one.
 #include "device_common.hpp"
+#include "launch.hpp"
 #include "launch_layer.hpp"
 
 namespace fp8lin {
@@ -22,13 +23,16 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 }
 
 // D / 16 lanes hold one head: two chunks of eight values each, which are the
-// two halves of eight pairs where the lane rotates.  A workgroup covers one
-// token, 256 * 16 / D heads at a time.
-template <int D>
-__global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
+// two halves of eight pairs where the lane rotates.  A workgroup covers 2^tokens_log2
+// tokens; a set of lanes keeps one token, with its angles in registers, and takes
+// its heads in strides of 256 16 / D >> tokens_log2.
+template <int D, bool FP8>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_log2) {
   constexpr int L = D / 16;
-  const int64_t token = blockIdx.x;
-  const int u = threadIdx.x % L;
+  const int u = threadIdx.x % L, set = threadIdx.x / L;
+  const int64_t token = ((int64_t)blockIdx.x << tokens_log2) + (set & ((1 << tokens_log2) - 1));
+  const int stride = 256 / L >> tokens_log2;
+  if (token >= a.T) return;  // whole sets of lanes
   const int heads = a.Hq + 2 * a.Hkv;
   const int turning = a.rot / 16;  // lanes of a head that rotate
   int c0, c1;                      // columns of the two chunks
@@ -39,23 +43,24 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     c0 = 8 * u;
     c1 = 8 * u + a.rot / 2;
   }
+  const uint16_t *row = a.qkv + token * heads * D;
+  const int64_t slot = a.slots[token];
   float cs[8], sn[8];
   if (u < turning) {
     const int p = min(max(a.positions[token], 0), a.max_pos - 1);
-    const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)p * a.rot + 8 * u);
-    const float4 *row2 = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)p * a.rot + a.rot / 2 + 8 * u);
-    const float4 k0 = row[0], k1 = row[1], s0 = row2[0], s1 = row2[1];
+    const float4 *cosines = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)p * a.rot + 8 * u);
+    const float4 *sines = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)p * a.rot + a.rot / 2 + 8 * u);
+    const float4 k0 = cosines[0], k1 = cosines[1], s0 = sines[0], s1 = sines[1];
     cs[0] = k0.x; cs[1] = k0.y; cs[2] = k0.z; cs[3] = k0.w; cs[4] = k1.x; cs[5] = k1.y; cs[6] = k1.z; cs[7] = k1.w;
     sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
   }
-  const int64_t slot = a.slots[token];
   const bool stored = slot >= 0 && slot < (int64_t)a.n_slots;
   const uint32_t page = stored ? (uint32_t)slot / a.page_size : 0, off = stored ? (uint32_t)slot % a.page_size : 0;
-  for (int h = threadIdx.x / L; h < heads; h += 256 / L) {
-    const uint16_t *src = a.qkv + (token * heads + h) * D;
+  // turns, rounds and stores head h
+  auto use = [&](const uint4(&r)[2], int h) {
     float f0[8], f1[8];
-    unpack8(*reinterpret_cast<const uint4 *>(src + c0), f0);
-    unpack8(*reinterpret_cast<const uint4 *>(src + c1), f1);
+    unpack8(r[0], f0);
+    unpack8(r[1], f1);
     if (h < a.Hq + a.Hkv && u < turning) {
       if (a.interleaved) {
 #pragma unroll
@@ -79,12 +84,12 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
       uint16_t *dst = a.q_out + (token * a.Hq + h) * D;
       *reinterpret_cast<uint4 *>(dst + c0) = pack8(f0);
       *reinterpret_cast<uint4 *>(dst + c1) = pack8(f1);
-      continue;
+      return;
     }
     const bool value = h >= a.Hq + a.Hkv;
     const int kvh = h - a.Hq - (value ? a.Hkv : 0);
     const int64_t line = ((int64_t)page * a.Hkv + kvh) * a.page_size + off;
-    if (a.k_scale) {
+    if constexpr (FP8) {
       uint32_t m = 0;
 #pragma unroll
       for (int j = 0; j < 8; j++)
@@ -103,19 +108,52 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
       *reinterpret_cast<uint4 *>(dst + c0) = pack8(f0);
       *reinterpret_cast<uint4 *>(dst + c1) = pack8(f1);
     }
+  };
+  for (int h = set >> tokens_log2; h < heads; h += stride) {
+    const uint16_t *src = row + h * D;
+    const uint4 r[2] = {*reinterpret_cast<const uint4 *>(src + c0), *reinterpret_cast<const uint4 *>(src + c1)};
+    use(r, h);
   }
+}
+
+// Tokens of a workgroup (log2): the choice that leaves the fewest of its lanes
+// idle, among those that leave two workgroups for each compute unit.  8192 tokens
+// of 36 heads of 64 (bf16 cache): one token a workgroup 16.7 us, four 13.7, eight
+// (the choice) 13.3 to 14.6; of 48 heads of 128: one 35.6, two (the choice) 35.3,
+// four 37.6; 64 tokens: one 3.6, two 4.0, four 5.6 us.
+int tokens_log2(const AppendArgs &a, int cus) {
+  const int heads = a.Hq + 2 * a.Hkv, sets = 256 / (a.D / 16);
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int lg = 0; (sets >> lg) > 0; lg++) {
+    const int stride = sets >> lg;
+    const int64_t cost = ((int64_t)((heads + stride - 1) / stride) << 16) >> lg;  // lane steps of a token
+    if (lg > 0 && ((a.T >> lg) < 2 * cus || cost >= best_cost)) continue;
+    best = lg;
+    best_cost = cost;
+  }
+  return best;
+}
+
+template <int D>
+void launch_append(const AppendArgs &a, hipStream_t stream) {
+  const int lg = tokens_log2(a, device_cu_count());
+  const dim3 grid((unsigned)((a.T + (1 << lg) - 1) >> lg)), block(256);
+  if (a.k_scale)
+    hipLaunchKernelGGL((append_kernel<D, true>), grid, block, 0, stream, a, lg);
+  else
+    hipLaunchKernelGGL((append_kernel<D, false>), grid, block, 0, stream, a, lg);
 }
 
 }  // namespace
 
 hipError_t launch_kv_rope_append(const AppendArgs &a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.T), block(256);
   if (a.D == 64)
-    hipLaunchKernelGGL(append_kernel<64>, grid, block, 0, stream, a);
+    launch_append<64>(a, stream);
   else if (a.D == 128)
-    hipLaunchKernelGGL(append_kernel<128>, grid, block, 0, stream, a);
+    launch_append<128>(a, stream);
   else
-    hipLaunchKernelGGL(append_kernel<256>, grid, block, 0, stream, a);
+    launch_append<256>(a, stream);
   return hipGetLastError();
 }
 
