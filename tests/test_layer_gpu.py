@@ -303,6 +303,9 @@ def paged(r, lens, Hkv, D, page, fp8, window, spare=3, pages=None):
 def attend_case(lib, lens, Hq, Hkv, D, page, fp8, window=0, softcap=0.0, max_len=None, sharp=1.5, pages=None, scale=None):
     r = gen(len(lens), sum(lens), Hq, Hkv, D, page, window)
     dev, table_, live = paged(r, lens, Hkv, D, page, fp8, window, pages=pages)
+    if max_len is not None and table_.shape[1] * page < max_len:  # a wider table, its entries out of range
+        more = -(-max_len // page) - table_.shape[1]
+        table_ = torch.cat([table_, torch.full((len(lens), more), -9, dtype=torch.int32, device="cuda")], 1)
     q = ref.bf16(sharp * r.standard_normal((len(lens), Hq, D)))
     call = lib.paged_decode_attention_fp8 if fp8 else lib.paged_decode_attention
     args = (q.cuda(), *dev, table_, torch.tensor(lens, dtype=torch.int32, device="cuda"))
@@ -348,6 +351,30 @@ def test_attention_window_and_cap(gpu_lib, window, softcap, fp8):
                                                 ([4097], 1, 1, 128, 4096)])
 def test_attention_long(gpu_lib, lens, Hq, Hkv, D, page, fp8):
     attend_case(gpu_lib, lens, Hq, Hkv, D, page, fp8)
+
+
+def ragged(kind):
+    r = gen("ragged", kind)
+    if kind == "few long among short":
+        return [int(x) for x in np.where(r.random(150) < 0.05, r.integers(500, 3000, 150), r.integers(0, 90, 150))]
+    if kind == "all one":
+        return [1] * 70
+    if kind == "one long":
+        return [40, 9000]
+    if kind == "fewer tiles than waves":
+        return [3, 0, 64]
+    return [int(x) for x in 2 ** r.uniform(0, 11, 67)]  # spread over the logarithm
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,page,window", [(32, 8, 128, 16, 0), (20, 1, 128, 48, 0), (6, 3, 64, 16, 1500),
+                                                  (36, 2, 64, 16, 0), (8, 2, 256, 32, 0)])
+@pytest.mark.parametrize("kind", ["few long among short", "all one", "one long", "fewer tiles than waves", "spread"])
+def test_attention_ragged(gpu_lib, kind, Hq, Hkv, D, page, window, fp8):
+    """Batches whose work is divided over the workgroups in even shares (a host bound of 4096 tokens or more): shares
+    with many rows, rows with many shares, and shares without work."""
+    lens = ragged(kind)
+    attend_case(gpu_lib, lens, Hq, Hkv, D, page, fp8, window=window, max_len=max(4096, max(lens)))
 
 
 def test_attention_batch(gpu_lib):
