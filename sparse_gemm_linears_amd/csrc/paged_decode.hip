@@ -19,9 +19,9 @@
 // each finds its share from the lengths and takes the rows in it in turn, alone,
 // without barriers; twelve waves on a compute unit keep its loads going.  A wave
 // leaves a partial for the row that its share begins inside and for the one that it
-// ends inside, and join_kernel adds the partials of a row in order.  One sequence
-// alone, and batches that give each wave a tile at most, are divided by the grid,
-// without the search.  Rows of short sequences have a workgroup each (row_kernel).
+// ends inside, and join_kernel adds the partials of a row in order.  Short
+// sequences, one sequence alone, and batches that give each wave a tile at most are
+// divided by the grid, without the search (row_kernel).
 //
 // Layouts (v_mfma_f32_16x16x32_bf16: lane l, n = l % 16, g = l / 16):
 //   scores   A = K: row n is token n of a half tile, B = Q: column n is a query
@@ -275,18 +275,18 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int len) {
   return max(1, (len - first_token(len, a.window) + kTile - 1) / kTile);
 }
 
-// How work is divided.  per == 0: even shares; the rows of a sequence follow
-// each other (bands of query heads within a key head), and wave i of
-// 2^log2_parts takes units share_start(i) .. share_start(i + 1) - 1 of all.  A
-// unit is a tile, and one more for the end of each row, which costs about as much
-// (shares of equal tiles took 77 us on 64 sequences of 1 to 8192 tokens where
+// How work is divided.  row_waves > 0: by the grid, `splits` workgroups of so
+// many waves for each row, `per` tiles each (row_kernel).  Else in even shares: the
+// rows of a sequence follow each other (bands of query heads within a key head),
+// and wave i of 2^log2_parts takes units share_start(i) .. share_start(i + 1) - 1 of
+// all.  A unit is a tile, and one more for the end of each row, which costs about as
+// much (shares of equal tiles took 77 us on 64 sequences of 1 to 8192 tokens where
 // sequences of equal length took 63).
-// per > 0: each row has `splits` waves of `per` tiles.
-// row_waves > 0: each row has one workgroup of that many waves (row_kernel).
 struct Plan {
-  int row_waves;
-  int per, splits, log2_parts;
-  int waves;
+  int row_waves, splits;
+  int64_t per;
+  int log2_parts;
+  int owners;    // workgroups (row_kernel) or waves (shares): each has two slots for partials
   int64_t rows;  // of the batch
   bool by_row;   // whether the list of divided rows is indexed by row, or by share
 };
@@ -297,7 +297,7 @@ __device__ __forceinline__ int64_t share_start(int64_t i, int64_t total, int log
 }
 
 // A row that is divided (slot < 0: none): its parts are in `slot` and in slot 0 of
-// the waves that follow `owner`: `parts` of them in all, or (parts == 0) as many
+// the owners that follow `owner`: `parts` of them in all, or (parts == 0) as many
 // as have shares that start before row_end.
 struct Cut {
   int64_t total, row_end;
@@ -305,8 +305,7 @@ struct Cut {
   int owner, pad;
 };
 
-// Partials of one part of a row: o [16 RT][D], then m and l [16 RT] each.  Each
-// wave has two slots.
+// Partials of one part of a row: o [16 RT][D], then m and l [16 RT] each.
 __host__ __device__ constexpr size_t part_floats(int D, int RT) { return (size_t)16 * RT * (D + 2); }
 
 // A unit of the batch: tile `tile` of row `band` of sequence b, or (tile ==
@@ -409,33 +408,23 @@ __device__ __forceinline__ Place find_unit(const DecodeArgs &a, int rows, int la
 }
 
 template <int D, bool FP8, int RT>
-__global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void decode_kernel(DecodeArgs a, Plan plan, float *part,
+__global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 2) void decode_kernel(DecodeArgs a, Plan plan, float *part,
                                                                            Cut *cuts) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int self = uniform((int)blockIdx.x * kWaves + (int)(threadIdx.x >> 6));
-  if (self >= plan.waves) return;
+  if (self >= plan.owners) return;
   const int group = a.Hq / a.Hkv, bands = (group + 16 * RT - 1) / (16 * RT), rows = a.Hkv * bands;
 
   Place at;      // the next tile to list
   int64_t left;  // units of the share that are not listed yet
   int64_t total = 0, position = 0;  // units of the batch, and where the share starts in them
-  if (plan.per > 0) {
-    const int row = self / plan.splits, split = self - row * plan.splits;
-    at.b = row / rows;
-    at.band = row - at.b * rows;
-    at.tile = split * plan.per;
-    at.len = uniform(length_of(a, at.b));
-    left = min(plan.per, tiles_of(a, at.len) - at.tile);
-    if (left <= 0) return;
-  } else {
-    int64_t before, upto;
-    total = batch_units(a, rows, lane, before, upto);
-    position = share_start(self, total, plan.log2_parts);
-    left = share_start(self + 1, total, plan.log2_parts) - position;
-    if (!plan.by_row && lane == 0) cuts[self].slot = -1;
-    if (left <= 0) return;  // there are more waves than units
-    at = find_unit(a, rows, lane, position, before, upto);
-  }
+  int64_t before, upto;
+  total = batch_units(a, rows, lane, before, upto);
+  position = share_start(self, total, plan.log2_parts);
+  left = share_start(self + 1, total, plan.log2_parts) - position;
+  if (!plan.by_row && lane == 0) cuts[self].slot = -1;
+  if (left <= 0) return;  // there are more waves than units
+  at = find_unit(a, rows, lane, position, before, upto);
   auto next_row = [&] {
     at.tile = 0;
     if (++at.band == rows) {
@@ -552,9 +541,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
           }
         }
         if (lane == 0 && row_begin == 0 && (plan.by_row || !whole)) {
-          const int parts = plan.per > 0 ? (tiles + plan.per - 1) / plan.per : 0;
           cuts[plan.by_row ? (int64_t)b * rows + band : (int64_t)self] =
-              Cut{total, row_position + tiles, b, band, whole ? -1 : slot, parts, self, 0};
+              Cut{total, row_position + tiles, b, band, whole ? -1 : slot, 0, self, 0};
         }
         fresh = true;
         started = false;
@@ -565,31 +553,42 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 1) void de
   }
 }
 
-// One row a workgroup, for short sequences: wave w takes tiles w, w + WAVES, ...
-// and the waves' states are added through LDS, in a fixed order.
+// A row's tiles divided by the grid: workgroup `split` of a row takes tiles per split
+// .. per split + per - 1, its waves every WAVES-th of them, and the waves' states
+// are added through LDS, in a fixed order.
 template <int D, bool FP8, int RT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void row_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 2) void row_kernel(DecodeArgs a, Plan plan, float *part, Cut *cuts) {
   constexpr int kPad = D + 4;  // a head in LDS, off the bank period
   extern __shared__ __align__(16) float box[];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
   const int group = a.Hq / a.Hkv, rows = a.Hkv * ((group + 16 * RT - 1) / (16 * RT));
-  const int b = (int)blockIdx.x / rows;
-  const Row row(a, b, (int)blockIdx.x - b * rows, RT);
+  const int row_at = (int)blockIdx.x / plan.splits, split = (int)blockIdx.x - row_at * plan.splits;
+  const int b = row_at / rows, band = row_at - b * rows;
+  const Row row(a, b, band, RT);
   float *box_m = box, *box_l = box_m + WAVES * row.heads, *box_o = box_l + WAVES * row.heads;  // 32 heads bytes apart
   v8bf qf[RT][D / 32];
   load_queries<D, FP8, RT>(qf, a, row, n, g);
-  // lane x looks up the half tiles of the wave's tile x; without a window before the length is known
-  const int mine = kTile * (wave + WAVES * (lane >> 1)) + 16 * (lane & 1);
-  int64_t early = 0;
-  if (a.window == 0 && mine < a.max_len) early = line_of(a, b, row.kvh, mine);
+  // Lane x looks up half tile x % 2 of the wave's tile x / 2; without a window
+  // before the length is known (which takes as long).
+  const int64_t begin = split * plan.per;
+  const int64_t mine = kTile * (begin + wave + WAVES * (lane >> 1)) + 16 * (lane & 1);
+  int64_t found = 0;
+  if (a.window == 0 && mine < a.max_len) found = line_of(a, b, row.kvh, (int)mine);
   const int len = uniform(length_of(a, b)), first = first_token(len, a.window), tiles = tiles_of(a, len);
-  if (a.window > 0 && first + mine < len) early = line_of(a, b, row.kvh, first + mine);
+  if (begin >= tiles) return;
+  const int end = (int)min((int64_t)tiles, begin + plan.per);
+  if (a.window > 0 && first + mine < len) found = line_of(a, b, row.kvh, (int)(first + mine));
   State<D> st[RT];
   clear_state(st);
-  for (int i = wave, x = 0; i < tiles && len > 0; i += WAVES, x++) {
+  for (int i = (int)begin + wave, x = 0; i < end && len > 0; i += WAVES, x++) {
     const int token = first + kTile * i;
+    if (x == 32) {  // the next 32 tiles
+      x = 0;
+      const int ahead = token + kTile * WAVES * (lane >> 1) + 16 * (lane & 1);
+      found = ahead < len ? line_of(a, b, row.kvh, ahead) : 0;
+    }
     // a half tile past the end counts for nothing: any line will do
-    const int64_t line[2] = {from_lane(early, 2 * x), token + 16 < len ? from_lane(early, 2 * x + 1) : 0};
+    const int64_t line[2] = {from_lane(found, 2 * x), token + 16 < len ? from_lane(found, 2 * x + 1) : 0};
     Tile<D, FP8> t;
     load_tile<D, FP8>(t, a, line, n, g);
     use_tile<D, FP8, RT>(t, a, qf, st, token, a.window > 0 ? max(0, len - a.window) : 0, len, g);
@@ -615,6 +614,8 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void row_kernel(Decod
     }
   }
   __syncthreads();
+  const bool whole = begin == 0 && end == tiles;
+  float *base = part + 2 * (size_t)blockIdx.x * part_floats(D, RT);
   for (int c = threadIdx.x; c < row.heads * (D / 4); c += 64 * WAVES) {
     const int head = c / (D / 4), d = c % (D / 4) * 4;
     float top = -INFINITY, l = 0.f, o[4] = {};
@@ -630,11 +631,22 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void row_kernel(Decod
       o[2] += x.z * f;
       o[3] += x.w * f;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2 *>(a.o + (row.q0 + head) * D + d) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    if (a.lse && d == 0) a.lse[row.q0 + head] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2 *>(a.o + (row.q0 + head) * D + d) =
+          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+      if (a.lse && d == 0) a.lse[row.q0 + head] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+    } else {
+      *reinterpret_cast<float4 *>(base + head * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+      if (d == 0) {
+        base[16 * RT * D + head] = top;
+        base[16 * RT * (D + 1) + head] = l;
+      }
+    }
   }
+  if (plan.splits > 1 && split == 0 && threadIdx.x == 0)
+    cuts[row_at] = Cut{0, 0, b, band, whole ? -1 : 2 * (int)blockIdx.x, (int)((tiles + plan.per - 1) / plan.per),
+                       (int)blockIdx.x, 0};
 }
 
 // Joins the parts of divided rows, in a fixed order.  Workgroup (i, y) takes row i
@@ -743,38 +755,36 @@ Plan plan_decode(const DecodeArgs &a, int cus) {
   const int wide = 16 * row_tiles(a);
   Plan p{};
   p.rows = (int64_t)a.B * a.Hkv * ((a.Hq / a.Hkv + wide - 1) / wide);
-  // Short sequences: a workgroup for each row and no second kernel.  Measured
-  // (GPU time, 32 query and 8 key heads of 128, bf16) against the divided forms:
-  // one sequence of 300 tokens 7.1 us against 8.6, 16 of up to 500 9.3 / 12.4, 128
-  // of up to 500 23.2 / 27.7; with 25 tiles 10.7 / 8.9 for one sequence (one
-  // compute unit's loads bound it), with 32 16.7 / 21.1 for 32 sequences.
-  if (tiles <= (p.rows < 64 ? 16 : 32)) {
-    p.row_waves = a.D <= 128 && wide == 16 && p.rows <= cus ? 8 : 4;
-    return p;
-  }
   // Waves that are resident together; fewer where a wave's tiles would be few
   // beside the partials that it leaves (32 query heads on one key head of 128, 16
   // sequences of 4000 to 8000 tokens: 2048 waves 36 us, 1024 27 us).
   const int heads = a.Hq / a.Hkv < wide ? a.Hq / a.Hkv : wide;
   const int64_t resident = (a.D <= 128 ? 8 : 4) * cus, fed = p.rows * tiles * 8 / heads;
   const int64_t parts = resident < fed ? resident : fed > 512 ? fed : 512;
-  if (a.B == 1 || p.rows * tiles <= parts) {
-    p.per = (int)((p.rows * tiles + parts - 1) / parts);
+  // Short sequences: a workgroup for each row and no second kernel.  Measured
+  // (GPU time, 32 query and 8 key heads of 128, bf16) against the divided forms:
+  // one sequence of 300 tokens 7.1 us against 8.6, 16 of up to 500 9.3 / 12.4, 128
+  // of up to 500 23.2 / 27.7; with 25 tiles 10.7 / 8.9 for one sequence (one
+  // compute unit's loads bound it), with 32 16.7 / 21.1 for 32 sequences.
+  const bool small = tiles <= (p.rows < 64 ? 16 : 32);
+  if (small || a.B == 1 || p.rows * tiles <= parts) {
+    // more waves of a workgroup join through LDS where rows have work for them: 4000
+    // tokens of one sequence 9.8 us with four and 11.0 with eight, 131072 89.3 / 88.1
+    p.row_waves = a.D <= 128 && wide == 16 && (small ? p.rows <= cus : p.rows * tiles > parts) ? 8 : 4;
+    p.per = small ? tiles : p.row_waves * ((p.rows * tiles + parts - 1) / parts);
     p.splits = (int)((tiles + p.per - 1) / p.per);
-  }
-  if (p.per > 0) {
-    p.waves = (int)(p.rows * p.splits);
+    p.owners = (int)(p.rows * p.splits);
     p.by_row = p.splits > 1;
     return p;
   }
   while ((int64_t)3 << p.log2_parts <= 2 * parts) p.log2_parts++;  // the nearest power of two
-  p.waves = 1 << p.log2_parts;
-  p.by_row = p.rows <= p.waves;
+  p.owners = 1 << p.log2_parts;
+  p.by_row = p.rows <= p.owners;
   return p;
 }
 
 template <int D, bool FP8, int RT, int WAVES>
-hipError_t launch_row(const DecodeArgs &a, const Plan &p, hipStream_t stream) {
+hipError_t launch_row(const DecodeArgs &a, const Plan &p, float *part, Cut *cuts, hipStream_t stream) {
   const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
   const size_t lds = (size_t)WAVES * heads * (D + 6) * sizeof(float);
   auto *kernel = row_kernel<D, FP8, RT, WAVES>;
@@ -783,28 +793,31 @@ hipError_t launch_row(const DecodeArgs &a, const Plan &p, hipStream_t stream) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)p.rows), dim3(64 * WAVES), lds, stream, a);
-  return hipGetLastError();
+  hipLaunchKernelGGL(kernel, dim3((unsigned)p.owners), dim3(64 * WAVES), lds, stream, a, p, part, cuts);
+  return hipSuccess;
 }
 
 template <int D, bool FP8, int RT>
 hipError_t launch_decode(const DecodeArgs &a, const Plan &p, float *part, hipStream_t stream) {
+  Cut *cuts = reinterpret_cast<Cut *>(part + 2 * (size_t)p.owners * part_floats(D, RT));
+  hipError_t e = hipSuccess;
+  if (p.row_waves == 4) e = launch_row<D, FP8, RT, 4>(a, p, part, cuts, stream);
   if constexpr (D <= 128 && RT == 1) {
-    if (p.row_waves == 8) return launch_row<D, FP8, RT, 8>(a, p, stream);
+    if (p.row_waves == 8) e = launch_row<D, FP8, RT, 8>(a, p, part, cuts, stream);
   }
-  if (p.row_waves) return launch_row<D, FP8, RT, 4>(a, p, stream);
-  Cut *cuts = reinterpret_cast<Cut *>(part + 2 * (size_t)p.waves * part_floats(D, RT));
-  hipLaunchKernelGGL((decode_kernel<D, FP8, RT>), dim3((unsigned)((p.waves + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                     stream, a, p, part, cuts);
-  if (p.per == 0 || p.splits > 1) {
+  if (e != hipSuccess) return e;
+  if (!p.row_waves)
+    hipLaunchKernelGGL((decode_kernel<D, FP8, RT>), dim3((unsigned)((p.owners + kWaves - 1) / kWaves)), dim3(kThreads),
+                       0, stream, a, p, part, cuts);
+  if (!p.row_waves || p.splits > 1) {
     const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
-    const unsigned listed = (unsigned)(p.by_row ? p.rows : p.waves);
+    const unsigned listed = (unsigned)(p.by_row ? p.rows : p.owners);
     // many (row, head) pairs: four heads a workgroup (2048 pairs of 5 parts: 8.1 us with a workgroup for each, 5.1
     // so); few: one, with more waves where a row has many parts (32 pairs of 25 parts: 8.3 us with four, 3.6 so)
     if (p.rows * heads > 1024)
       hipLaunchKernelGGL((join_kernel<D, RT, 4, 4>), dim3(listed, (unsigned)((heads + 3) / 4)), dim3(256), 0, stream, a,
                          p.log2_parts, (const float *)part, (const Cut *)cuts);
-    else if (p.rows * 64 > p.waves)
+    else if (p.rows * 64 > p.owners)
       hipLaunchKernelGGL((join_kernel<D, RT, 4, 1>), dim3(listed, (unsigned)heads), dim3(256), 0, stream, a,
                          p.log2_parts, (const float *)part, (const Cut *)cuts);
     else
@@ -831,9 +844,9 @@ hipError_t launch_dim(const DecodeArgs &a, const Plan &p, float *part, hipStream
 
 size_t paged_decode_partial_bytes(const DecodeArgs &a, int cus) {
   const Plan p = plan_decode(a, cus);
-  if (p.row_waves || (p.per > 0 && p.splits == 1)) return 0;
-  return 2 * (size_t)p.waves * part_floats(a.D, row_tiles(a)) * sizeof(float) +
-         (size_t)(p.by_row ? p.rows : p.waves) * sizeof(Cut);
+  if (p.row_waves && p.splits == 1) return 0;
+  return 2 * (size_t)p.owners * part_floats(a.D, row_tiles(a)) * sizeof(float) +
+         (size_t)(p.by_row ? p.rows : p.owners) * sizeof(Cut);
 }
 
 hipError_t launch_paged_decode(const DecodeArgs &a, float *part, hipStream_t stream) {
