@@ -62,7 +62,7 @@ def _link_marshal(obj: str) -> None:
 
     tmp = MARSHAL + ".tmp%d" % os.getpid()
     cmd = ["g++", "-shared", obj, "-o", tmp, "-L", HERE, "-l:libfp8lin.so",
-           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
            "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
