@@ -460,11 +460,11 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  * o are held in fp32; the softmax weights enter the product with v as two bf16
  * numbers each (17 bits).  Cache lines past a sequence's length or before its
  * window may hold anything.  Page numbers out of range are clamped: such rows
- * are unspecified, with no access outside the cache.  Where max_len is more than
- * 512 tokens the whole batch's tokens are divided evenly over the workgroups,
+ * are unspecified, with no access outside the cache.  Beyond short sequences rows
+ * are divided, or a ragged batch's tokens are divided evenly over the device,
  * with fp32 partials in library scratch memory that a second kernel joins in a
- * fixed order: results are deterministic, but a row's rounding depends on the
- * lengths beside it.  B <= 65535.
+ * fixed order: results are deterministic, but a row's rounding depends on max_len
+ * and in a ragged batch on the lengths beside it.  B <= 65535.
  */
 fp8l_status paged_decode_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                                    const int32_t *block_table, const int32_t *seq_lens, int64_t B, int64_t Hq,

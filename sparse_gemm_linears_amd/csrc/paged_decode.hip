@@ -20,8 +20,8 @@
 // without barriers; twelve waves on a compute unit keep its loads going.  A wave
 // leaves a partial for the row that its share begins inside and for the one that it
 // ends inside, and join_kernel adds the partials of a row in order.  Short
-// sequences, one sequence alone, and batches that give each wave a tile at most are
-// divided by the grid, without the search (row_kernel).
+// sequences, one sequence alone, windows, and batches that give each wave a few tiles
+// at most are divided by the grid, without the search (row_kernel).
 //
 // Layouts (v_mfma_f32_16x16x32_bf16: lane l, n = l % 16, g = l / 16):
 //   scores   A = K: row n is token n of a half tile, B = Q: column n is a query
@@ -767,7 +767,15 @@ Plan plan_decode(const DecodeArgs &a, int cus) {
   // of up to 500 23.2 / 27.7; with 25 tiles 10.7 / 8.9 for one sequence (one
   // compute unit's loads bound it), with 32 16.7 / 21.1 for 32 sequences.
   const bool small = tiles <= (p.rows < 64 ? 16 : 32);
-  if (small || a.B == 1 || p.rows * tiles <= parts) {
+  // The grid divides rows as if all were as long as the longest: no search, and one
+  // join of parts of a workgroup.  That is faster while a wave has a few tiles, and
+  // for windows, which make rows alike; ragged batches of more take even shares.
+  // (bf16, up to 2000 tokens: 8 equal sequences 17.0 us by the grid, 20.4 by shares,
+  // 8 of 100 on 13.9 / 16.5; up to 8000: 4 equal 26.4 / 31.1, 4 of 500 on 20.6 /
+  // 22.0, 8 of 500 on 32 / 28; a window of 1024 in 37 of 5 to 6000 22.6 / 26.7, of
+  // 4096 in 32 of 4000 to 9000 84 / 100, of 100 to 9000 65 / 64.)
+  const bool alike = a.window > 0 && a.window < a.max_len;
+  if (small || a.B == 1 || p.rows * tiles <= (alike ? 32 : 4) * parts) {
     // more waves of a workgroup join through LDS where rows have work for them: 4000
     // tokens of one sequence 9.8 us with four and 11.0 with eight, 131072 89.3 / 88.1
     p.row_waves = a.D <= 128 && wide == 16 && (small ? p.rows <= cus : p.rows * tiles > parts) ? 8 : 4;
