@@ -134,6 +134,24 @@ def test_norm_in_place_and_without_codes(gpu_lib):
         assert (a is None and b is None) or torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,K", [(8200, 7168), (16500, 3584)])
+def test_norm_large(gpu_lib, M, K):
+    """Inputs larger than the caches (read past them): sampled rows against the reference."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, res = (torch.randn(M, K, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = ref.bf16(1 + 0.2 * gen(K, "large").standard_normal(K))
+    h, y, q, s = gpu_lib.fp8_add_rmsnorm(x, w.cuda(), res, eps=1e-5, keep_y=True)
+    rows = torch.cat([torch.arange(0, M, 97), torch.tensor([M - 1])])
+    at = rows.cuda()
+    xs, rs = x[at].cpu(), res[at].cpu()
+    _, v = ref.norm(ref.f64(xs), ref.f64(rs), ref.f64(w), 1e-5)
+    assert torch.equal(h[at].cpu(), (xs.float() + rs.float()).bfloat16())
+    assert_rounded(y[at], v, 2.0 ** -18 * np.abs(v), "y")
+    groups, scale = v.reshape(len(rows), K // 128, 128), ref.f64(s[at])
+    holds(np.abs(scale - np.abs(groups).max(-1) / 448) <= 2.0 ** -18 * scale, "scales")
+    check_codes(q[at], scale, groups)
+
+
 def test_norm_special_rows(gpu_lib):
     """A zero row (eps keeps it zero), a row of tiny values, an infinity and a NaN: only their own rows are touched."""
     x = torch.ones(6, 512)
@@ -221,7 +239,8 @@ def append_case(lib, T, Hq, Hkv, D, rot, page, fp8, interleaved, pages=None, see
     (1, 32, 8, 128, 128, 16, False), (1, 1, 1, 64, 64, 16, True), (2, 28, 4, 128, 64, 48, False),
     (57, 32, 8, 128, 128, 64, True), (130, 6, 2, 64, 32, 32, False), (33, 16, 1, 256, 256, 16, False),
     (19, 5, 5, 256, 128, 80, True), (40, 7, 7, 64, 16, 16, False), (11, 8, 2, 128, 0, 16, False),
-    (9, 3, 1, 128, 112, 4096, True), (515, 40, 8, 128, 128, 128, False), (3, 71, 71, 64, 48, 16, False)])
+    (9, 3, 1, 128, 112, 4096, True), (2051, 28, 4, 64, 32, 48, True), (4100, 6, 2, 128, 128, 16, False),
+    (1537, 16, 1, 256, 128, 32, False), (515, 40, 8, 128, 128, 128, False), (3, 71, 71, 64, 48, 16, False)])
 def test_append(gpu_lib, T, Hq, Hkv, D, rot, page, interleaved, fp8):
     append_case(gpu_lib, T, Hq, Hkv, D, rot, page, fp8, interleaved)
 
@@ -371,10 +390,11 @@ def ragged(kind):
                                                   (36, 2, 64, 16, 0), (8, 2, 256, 32, 0)])
 @pytest.mark.parametrize("kind", ["few long among short", "all one", "one long", "fewer tiles than waves", "spread"])
 def test_attention_ragged(gpu_lib, kind, Hq, Hkv, D, page, window, fp8):
-    """Batches whose work is divided over the workgroups in even shares (a host bound of 4096 tokens or more): shares
+    """Batches whose work is divided over the workgroups in even shares (host bounds above the lengths): shares
     with many rows, rows with many shares, and shares without work."""
     lens = ragged(kind)
-    attend_case(gpu_lib, lens, Hq, Hkv, D, page, fp8, window=window, max_len=max(4096, max(lens)))
+    for bound in (max(4096, max(lens)), 1 << 17):  # by the grid for small batches, in even shares
+        attend_case(gpu_lib, lens, Hq, Hkv, D, page, fp8, window=window, max_len=bound)
 
 
 def test_attention_batch(gpu_lib):
@@ -457,14 +477,14 @@ def test_layer_graph_replay(gpu_lib):
     h, q = torch.empty_like(x), torch.empty(33, 4096, dtype=torch.uint8, device="cuda")
     s = torch.empty(33, 32, device="cuda")
     replay_equals_eager(lambda: gpu_lib.fp8_add_rmsnorm(x, w, res, h=h, q=q, s=s), [h, q, s])
-    r = gen("graph")
-    lens = [6000, 17, 0, 3000]
-    dev, table_, _ = paged(r, lens, 2, 128, 16, True, 0)
-    qq = ref.bf16(r.standard_normal((4, 8, 128))).cuda()
-    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    o, lse = torch.empty_like(qq), torch.empty(4, 8, device="cuda")
-    replay_equals_eager(lambda: gpu_lib.paged_decode_attention_fp8(qq, *dev, table_, seq, return_lse=True, o=o,
-                                                                   lse=lse), [o, lse])
+    for lens, Hkv in (([6000, 17, 0, 3000], 2), ([(61 * i) % 3000 for i in range(48)], 8)):  # by the grid, in shares
+        r = gen("graph", Hkv)
+        dev, table_, _ = paged(r, lens, Hkv, 128, 16, True, 0)
+        qq = ref.bf16(r.standard_normal((len(lens), 4 * Hkv, 128))).cuda()
+        seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        o, lse = torch.empty_like(qq), torch.empty(len(lens), 4 * Hkv, device="cuda")
+        replay_equals_eager(lambda: gpu_lib.paged_decode_attention_fp8(qq, *dev, table_, seq, return_lse=True, o=o,
+                                                                       lse=lse), [o, lse])
 
 
 def test_layer_on_side_streams(gpu_lib):
