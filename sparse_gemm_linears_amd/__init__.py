@@ -7,8 +7,8 @@ the library's HIP kernels.
 """
 from ._binding import (EXPORTS, FP8L_ERR_ALIAS, FP8L_ERR_ALIGN, FP8L_ERR_DEVICE, FP8L_ERR_LAUNCH, FP8L_ERR_MEMORY,
                        FP8L_ERR_NULL, FP8L_ERR_SCRATCH, FP8L_ERR_SHAPE, FP8L_OK, GROUP, LIB_PATH, MAX_LINEAR_M,
-                       Fp8LinError, fp8_add_rmsnorm, fp8_add_rmsnorm_ue8m0, fp8_block_gemm, fp8_block_gemm_noalloc, fp8_block_gemm_swiglu,
-                       fp8_block_gemm_ue8m0, fp8_block_linear, fp8_grouped_gemm,
+                       Fp8LinError, fp8_add_rmsnorm, fp8_add_rmsnorm_ue8m0, fp8_block_gemm, fp8_block_gemm_noalloc,
+                       fp8_block_gemm_swiglu, fp8_block_gemm_ue8m0, fp8_block_linear, fp8_grouped_gemm,
                        fp8_quant_act, fp8_quant_act_static, fp8_quant_act_tensor, fp8_quant_act_ue8m0,
                        fp8_quant_weight_block, fp8_quant_weight_block_ue8m0, fp8_quant_weight_tensor,
                        fp8_sparse24_gemm, fp8_sparse24_linear, fp8lin_release_graph_scratch, kv_rope_append,

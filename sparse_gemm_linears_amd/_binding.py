@@ -5,6 +5,9 @@ dtype / device / contiguity, allocates outputs unless ``out=`` tensors are
 given, and calls the C entry point on torch's current HIP stream.  Every step
 of the computation runs in the library's HIP kernels; there is no other code
 path, and a missing library is an error.
+
+The decoder-layer calls, which take microseconds, are marshalled by the
+extension module ``_marshal.so`` (csrc/marshal.cpp) instead of ctypes.
 """
 from __future__ import annotations
 
