@@ -152,6 +152,21 @@ def test_norm_large(gpu_lib, M, K):
     check_codes(q[at], scale, groups)
 
 
+@pytest.mark.parametrize("scales", ["fp32", "ue8m0"])
+def test_norm_more_rows_than_one_launch(gpu_lib, scales):
+    """More rows than one launch takes: repeated rows against a call of a few."""
+    M, K, period = (1 << 21) + 777, 128, 4096
+    x, res, w = (t.cuda() for t in norm_inputs(period, K, True, 5))
+    call = gpu_lib.fp8_add_rmsnorm if scales == "fp32" else gpu_lib.fp8_add_rmsnorm_ue8m0
+    want = call(x, w, res, keep_y=True)
+    times = -(-M // period)
+    got = call(x.repeat(times, 1)[:M], w, res.repeat(times, 1)[:M], keep_y=True)
+    for a, b in zip(got, want):
+        a, b = a.view(torch.uint8).view(M, -1), b.view(torch.uint8).view(period, -1)
+        whole = M // period * period
+        assert (a[:whole].view(-1, *b.shape) == b).all() and torch.equal(a[whole:], b[:M - whole])
+
+
 def test_norm_special_rows(gpu_lib):
     """A zero row (eps keeps it zero), a row of tiny values, an infinity and a NaN: only their own rows are touched."""
     x = torch.ones(6, 512)
@@ -352,7 +367,7 @@ EDGES = [0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 63, 64, 65, 100, 127, 128, 129, 25
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(32, 8, 128, 16), (28, 4, 64, 48), (16, 1, 256, 32), (3, 3, 128, 64),
                                            (40, 2, 128, 16), (33, 1, 64, 128), (64, 1, 128, 16), (70, 1, 256, 16),
-                                           (8, 8, 64, 16), (12, 4, 256, 1024)])
+                                           (8, 8, 64, 16), (10, 5, 256, 1024)])
 def test_attention_edges(gpu_lib, Hq, Hkv, D, page, fp8):
     attend_case(gpu_lib, EDGES, Hq, Hkv, D, page, fp8)
 
@@ -443,6 +458,22 @@ def test_attention_infinite_scores(gpu_lib):
     assert (o[1] == 0).all()
 
 
+def test_attention_more_rows_than_a_grid(gpu_lib):
+    """More than 2^24 rows (a sequence's key heads), all of one token or none: the token's value, or zeros."""
+    B, H, D, page = 65535, 257, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(11)
+    k, v = (torch.randn(3, H, page, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(H, D, generator=g, device="cuda").bfloat16().expand(B, H, D).contiguous()
+    pages = (torch.arange(B, dtype=torch.int32, device="cuda") % 3).view(B, 1).contiguous()
+    lens = (torch.arange(B, dtype=torch.int32, device="cuda") % 5 != 0).int()
+    o = gpu_lib.paged_decode_attention(q, k, v, pages, lens)
+    want = v[:, :, 0]
+    for b0 in range(0, B, 8192):  # in pieces, for memory
+        b1 = min(B, b0 + 8192)
+        piece = want[pages[b0:b1, 0].long()] * lens[b0:b1].view(-1, 1, 1)
+        assert (o[b0:b1] == piece).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_attention_and_append_past_32_bits(gpu_lib, fp8):
     """A cache of more than 2^32 elements, its last pages in use."""
@@ -452,13 +483,13 @@ def test_attention_and_append_past_32_bits(gpu_lib, fp8):
     kind = torch.uint8 if fp8 else torch.bfloat16
     k, v = (torch.empty(pages, 8, 16, 128, dtype=kind, device="cuda") for _ in range(2))
     sc = [torch.empty(pages, 8, 16, device="cuda") for _ in range(2)] if fp8 else []
-    qkv = ref.bf16(gen("far").standard_normal((2, 24 * 128))).cuda()
+    qkv = ref.bf16(gen("far").standard_normal((2, 32 * 128))).cuda()
     slots = torch.tensor([pages * 16 - 1, 5], device="cuda")
     cs = torch.from_numpy(table(4, 128)).cuda()
     pos = torch.zeros(2, dtype=torch.int32, device="cuda")
     (gpu_lib.kv_rope_append_fp8 if fp8 else gpu_lib.kv_rope_append)(qkv, pos, slots, cs, k, v, *sc)
-    rows = qkv.view(2, 24, 128)
-    for got, want in ((v[-1, :, 15], rows[0, 16:]), (v[0, :, 5], rows[1, 16:]), (k[-1, :, 15], rows[0, 8:16])):
+    rows = qkv.view(2, 32, 128)
+    for got, want in ((v[-1, :, 15], rows[0, 24:]), (v[0, :, 5], rows[1, 24:]), (k[-1, :, 15], rows[0, 16:24])):
         if fp8:
             s = want.float().abs().amax(-1, keepdim=True) / 448
             got = got.contiguous().view(torch.float8_e4m3fn).float() * s
