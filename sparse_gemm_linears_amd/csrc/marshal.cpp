@@ -113,11 +113,11 @@ void check(const char *fn, fp8l_status status) {
 // The C call, without the interpreter's lock.
 template <class Call>
 fp8l_status unlocked(Call call) {
-  fp8l_status st;
-  Py_BEGIN_ALLOW_THREADS
-  st = call();
-  Py_END_ALLOW_THREADS
-  return st;
+  struct Released {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }  // also when a tensor without storage throws
+  } released;
+  return call();
 }
 
 PyObject *wrap_or_none(const Tensor &t) {
