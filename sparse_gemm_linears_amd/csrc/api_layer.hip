@@ -116,6 +116,8 @@ fp8l_status decode(const DecodeArgs &in, int64_t B, int64_t Hq, int64_t Hkv, int
   a.max_pages = (int)max_pages;
   a.max_len = (int)max_len;
   a.window = (int)(window < kMaxSlots ? window : kMaxSlots);
+  // a smaller cap has no reciprocal, and leaves scores that no exponential tells from 0 either
+  if (a.softcap > 0.0f && a.softcap < 1e-30f) a.softcap = 1e-30f;
   CallScratch sc;
   if (hipError_t e = sc.acquire(paged_decode_partial_bytes(a, device_cu_count()), 0, stream)) return launched(e);
   const hipError_t e = launch_paged_decode(a, sc.partials(), stream);

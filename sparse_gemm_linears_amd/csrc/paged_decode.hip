@@ -190,12 +190,26 @@ __device__ __forceinline__ void use_tile(Tile<D, FP8> &t, const DecodeArgs &a, c
 #pragma unroll
     for (int j = 0; j < 8; j++) x[j] = s[r][j >> 2][j & 3] * factor[j];
     if (a.softcap > 0.f) {
-      // c tanh(x / c), with tanh z = 1 - 2 / (1 + exp 2z)
-      const float rate = 2.f * kLog2e / a.softcap;
+      // c tanh(x / c).  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that
+      // would lose a small score's low bits, its power series (2^-26 of it is left out).
+      const float rate = 1.f / a.softcap;
+      float z[8], most = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        const float e = __builtin_amdgcn_exp2f(x[j] * rate);
-        x[j] = a.softcap - 2.f * a.softcap * __builtin_amdgcn_rcpf(1.f + e);
+        z[j] = x[j] * rate;
+        const float u = z[j] * z[j];
+        float t = __builtin_fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+        t = __builtin_fmaf(u, t, 2.f / 15.f);
+        t = __builtin_fmaf(u, t, -1.f / 3.f);
+        x[j] = a.softcap * __builtin_fmaf(z[j] * u, t, z[j]);
+        most = fmaxf(most, fabsf(z[j]));
+      }
+      if (__any(most >= 0.25f)) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float m = fabsf(z[j]), e = __builtin_amdgcn_exp2f(2.f * kLog2e * m);
+          if (m >= 0.25f) x[j] = a.softcap * copysignf(1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e), z[j]);
+        }
       }
     }
 #pragma unroll

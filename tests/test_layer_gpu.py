@@ -9,7 +9,7 @@ Tolerances, from the number formats (u = 2^-24, half an fp32 ulp, relative):
 * append: a rotated value is within 4u (|a| + |b|) of the exact one, plus its
   output rounding; value heads are exact;
 * attention: with S the largest sum of scale |q_d k_d|, a score is within
-  (D + 8) u S (plus 2^-20 softcap for the tanh); o is within twice that, plus
+  (D + 8) u S (plus the tanh's: 2^-20 softcap, and 2^-19 of a score); o is within twice that, plus
   2^-16 for the two-part weights and u for each token of a chain, times
   sum p |v|; lse within the score's error, 2^-19 and u for each token.
 
@@ -353,7 +353,7 @@ def attend_case(lib, lens, Hq, Hkv, D, page, fp8, window=0, softcap=0.0, max_len
     for b, n in enumerate(lens):
         want, want_lse, spread, size = ref.attention(ref.f64(q[b]), *live[b], D ** -0.5 if scale is None else scale,
                                                      softcap)
-        score = (D + 8) * U * size + 2.0 ** -20 * softcap
+        score = (D + 8) * U * size + min(2.0 ** -20 * softcap, 2.0 ** -19 * size)
         assert_rounded(o[b], want, (2 * score + 2.0 ** -16 + n * U) * spread, f"o of row {b}, length {n}")
         if n == 0:
             assert (lse[b] == -np.inf).all()
@@ -377,6 +377,12 @@ def test_attention_edges(gpu_lib, Hq, Hkv, D, page, fp8):
                                             (0, 30.0), (1 << 40, 1.0)])
 def test_attention_window_and_cap(gpu_lib, window, softcap, fp8):
     attend_case(gpu_lib, EDGES + [1500, 2047, 3001], 14, 2, 128, 48, fp8, window=window, softcap=softcap)
+
+
+@pytest.mark.parametrize("softcap", [1e-40, 1e-3, 0.5, 300.0, 1e6, 1e30, 3e38])
+def test_attention_caps_of_any_size(gpu_lib, softcap):
+    """From caps that leave nothing of the scores to ones far above them, which change nothing."""
+    attend_case(gpu_lib, [1, 40, 700], 6, 2, 64, 16, False, softcap=softcap)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
