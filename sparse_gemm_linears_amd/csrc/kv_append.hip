@@ -118,20 +118,23 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_lo
   }
 }
 
-// Tokens of a workgroup (log2): the choice that leaves the fewest of its lanes
-// idle, among those that leave two workgroups for each compute unit.  8192 tokens
-// of 36 heads of 64 (bf16 cache): one token a workgroup 16.7 us, four 13.7, eight
-// (the choice) 13.3 to 14.6; of 48 heads of 128: one 35.6, two (the choice) 35.3,
-// four 37.6; 64 tokens: one 3.6, two 4.0, four 5.6 us.
+// Tokens of a workgroup (log2): more of them leave fewer of its lanes idle, but make
+// the workgroups fewer and their loops longer, so a number is taken if it needs a
+// fifth fewer lane steps than the last one taken, loops of five at most, and leaves
+// two workgroups for each compute unit.  With 1, 2, 4, 8, 16 tokens (* the choice): 12603
+// tokens of 34 heads of 64 (e4m3 cache) 22.0 20.1 19.4* 19.4 22.7 us, 9000 of 56 (bf16)
+// 26.6* 26.1 27.9 30.1 33.2, 30000 of 10 34.0 23.6 16.1 14.7 14.5*; of 128, 8192 of 48
+// 35.4 33.9* 36.4 36.2 37.0, 1100 of 48 7.2 7.1* 8.6 12.4 20.9, 600 of 48 5.3* 5.7 7.4 11.6.
 int tokens_log2(const AppendArgs &a, int cus) {
   const int heads = a.Hq + 2 * a.Hkv, sets = 256 / (a.D / 16);
   int best = 0;
   int64_t best_cost = 0;
   for (int lg = 0; (sets >> lg) > 0; lg++) {
     const int stride = sets >> lg;
-    const int64_t cost = ((int64_t)((heads + stride - 1) / stride) << 16) >> lg;  // lane steps of a token
+    const int steps = (heads + stride - 1) / stride;
+    const int64_t cost = ((int64_t)steps << 16) >> lg;  // lane steps of a token
     const bool fits = a.T >> best < 1 << 23;  // a grid's threads are counted in 32 bits
-    if (lg > 0 && fits && ((a.T >> lg) < 2 * cus || cost >= best_cost)) continue;
+    if (lg > 0 && fits && ((a.T >> lg) < 2 * cus || steps > 5 || 5 * cost > 4 * best_cost)) continue;
     best = lg;
     best_cost = cost;
   }
