@@ -280,7 +280,7 @@ constexpr int kListed = 64;  // tiles that a wave lists at a time, one in each l
 
 __host__ __device__ inline int first_token(int len, int window) {
   const int lo = window > 0 && len > window ? len - window : 0;
-  return lo & ~(kTile - 1);
+  return lo & ~15;  // a half tile lies in one page
 }
 
 __device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
@@ -771,7 +771,7 @@ int row_tiles(const DecodeArgs &a) { return a.Hq / a.Hkv <= 16 || a.D == 256 ? 1
 
 Plan plan_decode(const DecodeArgs &a, int cus) {
   int64_t tokens = a.max_len;  // live tokens of a sequence, from the tile that holds the first one
-  if (a.window > 0 && tokens > (int64_t)a.window + kTile) tokens = (int64_t)a.window + kTile;
+  if (a.window > 0 && tokens > (int64_t)a.window + 15) tokens = (int64_t)a.window + 15;
   const int64_t tiles = tokens <= kTile ? 1 : (tokens + kTile - 1) / kTile;
   const int wide = 16 * row_tiles(a);
   Plan p{};
@@ -782,12 +782,23 @@ Plan plan_decode(const DecodeArgs &a, int cus) {
   const int heads = a.Hq / a.Hkv < wide ? a.Hq / a.Hkv : wide;
   const int64_t resident = (a.D <= 128 ? 8 : 4) * cus, fed = p.rows * tiles * 8 / heads;
   const int64_t parts = resident < fed ? resident : fed > 512 ? fed : 512;
-  // Short sequences: a workgroup for each row and no second kernel.  Measured
-  // (GPU time, 32 query and 8 key heads of 128, bf16) against the divided forms:
-  // one sequence of 300 tokens 7.1 us against 8.6, 16 of up to 500 9.3 / 12.4, 128
-  // of up to 500 23.2 / 27.7; with 25 tiles 10.7 / 8.9 for one sequence (one
-  // compute unit's loads bound it), with 32 16.7 / 21.1 for 32 sequences.
-  const bool small = tiles <= (p.rows < 64 ? 16 : 32);
+  // Short sequences: a workgroup for each row and no second kernel, while the longest
+  // row takes one compute unit less time than dividing it costs; that is more when rows
+  // fill the device.  A tile costs its bytes and as much as 4 KiB beside them.  Whole / divided
+  // in us, by the longest row's tiles (32 query and 8 key heads; lengths from 1 on,
+  // crowding at the short ones, so that a whole row of the longest stands out):
+  //   of 128, bf16:  32 rows  8: 6.4 / 8.3, 16: 8.4 / 8.3, 24: 10.5 / 8.8
+  //                 128 rows 16: 9.3 / 11.3, 24: 12.6 / 13.8, 32: 15.7 / 13.7
+  //                 512 rows 24: 20.1 / 22.9, 32: 25.1 / 26.7, 48: 35.1 / 32.1
+  //   of 64, e4m3:   32 rows 24: 6.6 / 7.3, 32: 7.4 / 7.5, 48: 9.2 / 7.9
+  //                 256 rows 32: 8.8 / 12, 64: 12.9 / 16.4
+  //   of 256, bf16:  32 rows  8: 9.4 / 10.2, 16: 14.4 / 11.1
+  //                 256 rows 16: 20.3 / 20.2, 24: 27.4 / 24.5
+  const int tile_kb = 2 * kTile * a.D * (a.k_scale ? 1 : 2) / 1024;
+  const bool small = tiles * (tile_kb + 4) <= (p.rows < 64            ? 256
+                                               : p.rows < cus / 2     ? 336
+                                               : p.rows < cus / 4 * 3 ? 448
+                                                                      : 640);
   // The grid divides rows as if all were as long as the longest: no search, and one
   // join of parts of a workgroup.  That is faster while a wave has a few tiles, and
   // for windows, which make rows alike; ragged batches of more take even shares.
@@ -799,9 +810,14 @@ Plan plan_decode(const DecodeArgs &a, int cus) {
   if (small || a.B == 1 || p.rows * tiles <= (alike ? 32 : 4) * parts) {
     // more waves of a workgroup join through LDS where rows have work for them: 4000
     // tokens of one sequence 9.8 us with four and 11.0 with eight, 131072 89.3 / 88.1
-    p.row_waves = a.D <= 128 && wide == 16 && (small ? p.rows <= cus : p.rows * tiles > parts) ? 8 : 4;
-    // no waves without a tile: 200 sequences of up to 30 tokens 11.2 us with four, 8.1 with one
-    while (p.row_waves > tiles) p.row_waves /= 2;
+    // (short: 512 rows of 8 to 48 tiles 9.8 to 33.8 us with eight, 8.9 to 33.0 with four; but windows
+    // of 1024 in 592 rows of 64 22.4 / 25.6, in 1024 rows of 128 75.6 / 78.1).
+    const bool few = small && (!alike || tiles <= 16);
+    p.row_waves = a.D <= 128 && wide == 16 && (few ? p.rows <= cus : p.rows * tiles > parts) ? 8 : 4;
+    // no waves without a tile: 200 sequences of up to 30 tokens 11.2 us with four, 8.1 with one;
+    // but for three tiles four in few rows (8 rows 4.7 / 5.0 with two, 256 5.5 / 6.1, 1024 of 256
+    // 21.3 / 19.4), and two that write 32 heads (16 rows of 18 tokens 7.4, with one 8.2)
+    while (p.row_waves > (p.rows <= cus ? 2 * tiles - 1 : tiles) * (wide / 16)) p.row_waves /= 2;
     p.per = small ? tiles : p.row_waves * ((p.rows * tiles + parts - 1) / parts);
     p.splits = (int)((tiles + p.per - 1) / p.per);
     p.owners = (int)(p.rows * p.splits);
