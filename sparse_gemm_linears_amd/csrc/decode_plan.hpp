@@ -42,6 +42,21 @@ __host__ __device__ inline int64_t share_start(int64_t i, int64_t total, int log
 // Partials of one part of a row: o [16 RT][D], then m and l [16 RT] each.
 __host__ __device__ constexpr size_t part_floats(int D, int RT) { return (size_t)16 * RT * (D + 2); }
 
+// LDS of a row_kernel workgroup, offsets in floats: o of each wave's heads, kHead floats
+// each, then m and l.  o comes first because it is read and written 16 bytes at a time:
+// behind the 8 n bytes of m and l it would start off 16 bytes for an odd n.
+struct RowBox {
+  int o, m, l, floats;
+};
+template <int D>
+struct RowBoxOf {
+  static constexpr int kHead = D + 4;  // off the bank period, whole 16 bytes
+  static __host__ __device__ constexpr RowBox at(int waves, int heads) {
+    const int n = waves * heads;
+    return RowBox{0, n * kHead, n * kHead + n, n * (kHead + 2)};
+  }
+};
+
 // Sets of 16 query heads that a row holds: two where a key head has more than 16,
 // so that its lines are read once for up to 32 (not for D = 256, whose state of
 // two sets leaves no registers for the tiles).

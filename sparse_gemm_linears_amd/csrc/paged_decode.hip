@@ -547,8 +547,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? (RT == 1 ? 3 : 2) : 2) void de
 // are added through LDS, in a fixed order.
 template <int D, bool FP8, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void row_kernel(DecodeArgs a, DecodePlan plan, float *part, Cut *cuts) {
-  constexpr int kPad = D + 4;  // a head in LDS, off the bank period
-  extern __shared__ __align__(16) float box[];
+  constexpr int kPad = RowBoxOf<D>::kHead;
+  extern __shared__ __align__(16) float lds[];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
   const int group = a.Hq / a.Hkv, rows = a.Hkv * ((group + 16 * RT - 1) / (16 * RT));
   int row_at = (int)blockIdx.x / plan.splits;
@@ -556,7 +556,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void row_kernel(DecodeArgs a, Decode
   row_at += plan.first_row;
   const int b = row_at / rows, band = row_at - b * rows;
   const Row row(a, b, band, RT);
-  float *box_m = box, *box_l = box_m + WAVES * row.heads, *box_o = box_l + WAVES * row.heads;  // 32 heads bytes apart
+  const RowBox box = RowBoxOf<D>::at(WAVES, row.heads);
+  float *box_o = lds + box.o, *box_m = lds + box.m, *box_l = lds + box.l;
   v8bf qf[RT][D / 32];
   load_queries<D, FP8, RT>(qf, a, row, n, g);
   // Lane x looks up half tile x % 2 of the wave's tile x / 2; without a window
@@ -737,7 +738,7 @@ __global__ __launch_bounds__(64 * WAVES) void join_kernel(DecodeArgs a, int log2
 template <int D, bool FP8, int RT, int WAVES>
 hipError_t launch_row(const DecodeArgs &a, const DecodePlan &p, float *part, Cut *cuts, hipStream_t stream) {
   const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
-  const size_t lds = (size_t)WAVES * heads * (D + 6) * sizeof(float);
+  const size_t lds = (size_t)RowBoxOf<D>::at(WAVES, heads).floats * sizeof(float);
   auto *kernel = row_kernel<D, FP8, RT, WAVES>;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
