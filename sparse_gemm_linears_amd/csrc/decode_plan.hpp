@@ -62,6 +62,14 @@ struct RowBoxOf {
 // two sets leaves no registers for the tiles).
 inline int row_tiles(const DecodeArgs &a) { return a.Hq / a.Hkv <= 16 || a.D == 256 ? 1 : 2; }
 
+// Whether row_kernel exists for this many waves of a workgroup (a plan asks for no other).
+constexpr bool has_row_form(int D, int RT, int waves) {
+  return (waves == 1 && RT == 1) || waves == 2 || waves == 4 || (waves == 8 && D <= 128 && RT == 1);
+}
+
+// Workgroups of one row_kernel launch: a grid counts its threads in 32 bits.
+constexpr int kRowGrid = 1 << 22;
+
 inline DecodePlan plan_decode(const DecodeArgs &a, int cus) {
   int64_t tokens = a.max_len;  // live tokens of a sequence, from the tile that holds the first one
   if (a.window > 0 && tokens > (int64_t)a.window + 15) tokens = (int64_t)a.window + 15;

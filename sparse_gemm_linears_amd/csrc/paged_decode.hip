@@ -745,11 +745,9 @@ hipError_t launch_row(const DecodeArgs &a, const DecodePlan &p, float *part, Cut
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  // a grid counts its threads in 32 bits: more rows (never divided) go in several launches
-  constexpr int kGrid = 1 << 22;
-  DecodePlan q = p;
-  for (; p.owners - q.first_row > kGrid; q.first_row += kGrid)
-    hipLaunchKernelGGL(kernel, dim3((unsigned)kGrid), dim3(64 * WAVES), lds, stream, a, q, part, cuts);
+  DecodePlan q = p;  // more rows than a grid takes (never divided ones) go in several launches
+  for (; p.owners - q.first_row > kRowGrid; q.first_row += kRowGrid)
+    hipLaunchKernelGGL(kernel, dim3((unsigned)kRowGrid), dim3(64 * WAVES), lds, stream, a, q, part, cuts);
   hipLaunchKernelGGL(kernel, dim3((unsigned)(p.owners - q.first_row)), dim3(64 * WAVES), lds, stream, a, q, part, cuts);
   return hipSuccess;
 }
@@ -757,17 +755,21 @@ hipError_t launch_row(const DecodeArgs &a, const DecodePlan &p, float *part, Cut
 template <int D, bool FP8, int RT>
 hipError_t launch_decode(const DecodeArgs &a, const DecodePlan &p, float *part, hipStream_t stream) {
   Cut *cuts = reinterpret_cast<Cut *>(part + 2 * (size_t)p.owners * part_floats(D, RT));
-  hipError_t e = hipSuccess;
-  if (p.row_waves == 1) e = launch_row<D, FP8, RT, 1>(a, p, part, cuts, stream);
+  hipError_t e = hipErrorInvalidValue;  // a form that is not built
+  if (p.row_waves == 0) {
+    hipLaunchKernelGGL((decode_kernel<D, FP8, RT>), dim3((unsigned)((p.owners + kWaves - 1) / kWaves)), dim3(kThreads),
+                       0, stream, a, p, part, cuts);
+    e = hipSuccess;
+  }
+  if constexpr (has_row_form(D, RT, 1)) {
+    if (p.row_waves == 1) e = launch_row<D, FP8, RT, 1>(a, p, part, cuts, stream);
+  }
   if (p.row_waves == 2) e = launch_row<D, FP8, RT, 2>(a, p, part, cuts, stream);
   if (p.row_waves == 4) e = launch_row<D, FP8, RT, 4>(a, p, part, cuts, stream);
-  if constexpr (D <= 128 && RT == 1) {
+  if constexpr (has_row_form(D, RT, 8)) {
     if (p.row_waves == 8) e = launch_row<D, FP8, RT, 8>(a, p, part, cuts, stream);
   }
   if (e != hipSuccess) return e;
-  if (!p.row_waves)
-    hipLaunchKernelGGL((decode_kernel<D, FP8, RT>), dim3((unsigned)((p.owners + kWaves - 1) / kWaves)), dim3(kThreads),
-                       0, stream, a, p, part, cuts);
   if (!p.row_waves || p.splits > 1) {
     const int group = a.Hq / a.Hkv, heads = group < 16 * RT ? group : 16 * RT;
     const unsigned listed = (unsigned)(p.by_row ? p.rows : p.owners);

@@ -19,5 +19,5 @@ def driver(tmp_path_factory):
     return exe
 
 
-def test_layouts(driver):
+def test_plans_and_layouts(driver):
     assert "decode plan driver: ok" in _run([driver]).stdout
