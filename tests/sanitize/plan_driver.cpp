@@ -1,6 +1,7 @@
 // Driver for the attention's launch plan and layouts (decode_plan.hpp), on the host
 // alone (test infrastructure).
 #include <cstdio>
+#include <cstdlib>
 
 #include "../../sparse_gemm_linears_amd/csrc/decode_plan.hpp"
 
@@ -109,7 +110,24 @@ static void plans() {
   std::printf("attention plans: %ld\n", checked);
 }
 
-int main() {
+// Arguments B Hq Hkv D e4m3 max_len window: prints the plan for 256 compute units.
+static int one(char **v) {
+  float scale = 0.f;
+  DecodeArgs a{};
+  a.B = std::atoi(v[0]);
+  a.Hq = std::atoi(v[1]);
+  a.Hkv = std::atoi(v[2]);
+  a.D = std::atoi(v[3]);
+  if (std::atoi(v[4])) a.k_scale = a.v_scale = &scale;
+  a.max_len = std::atoi(v[5]);
+  a.window = std::atoi(v[6]);
+  const DecodePlan p = plan_decode(a, 256);
+  std::printf("%d %d %d\n", p.row_waves, p.splits, (int)p.by_row);
+  return 0;
+}
+
+int main(int argc, char **argv) {
+  if (argc == 8) return one(argv + 1);
   plans();
   boxes<64>();
   boxes<128>();

@@ -6,6 +6,7 @@ import os
 
 import pytest
 
+from decode_forms import BATCHES
 from test_sanitize_cpu import CLANGXX, HERE, _run
 
 
@@ -21,3 +22,17 @@ def driver(tmp_path_factory):
 
 def test_plans_and_layouts(driver):
     assert "decode plan driver: ok" in _run([driver]).stdout
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch", BATCHES, ids=lambda b: b.name)
+def test_batches_reach_their_forms(driver, batch, fp8):
+    """Each batch of test_decode_forms_gpu.py takes the form it is there for, whatever the plan's thresholds are."""
+    args = (batch.B, batch.Hq, batch.Hkv, batch.D, int(fp8), batch.max_len, batch.window)
+    waves, splits, by_row = (int(x) for x in _run([driver, *map(str, args)]).stdout.split())
+    if waves:
+        assert batch.form == ("rows", waves, splits > 1)
+    else:
+        assert batch.form == ("shares", "listed by row" if by_row else "by share")
+    assert len(batch.lens()) == batch.B and max(batch.lens()) <= batch.max_len
+    assert not batch.window or batch.window >= 1000 or max(batch.lens()) > batch.window
