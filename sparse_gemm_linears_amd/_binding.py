@@ -7,7 +7,8 @@ of the computation runs in the library's HIP kernels; there is no other code
 path, and a missing library is an error.
 
 The decoder-layer calls, which take microseconds, are marshalled by the
-extension module ``_marshal.so`` (csrc/marshal.cpp) instead of ctypes.
+extension module ``_marshal.so`` (csrc/marshal.cpp) instead of ctypes; only they
+need it.
 """
 from __future__ import annotations
 
@@ -54,15 +55,19 @@ class Fp8LinError(RuntimeError):
         self.status = status
 
 
+def _require(path: str):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build() "
+                           "or python sparse_gemm_linears_amd/build.py")
+
+
 def load_library():
     """Load ``libfp8lin.so``; raises if it has not been built."""
     global _lib
     with _lock:
         if _lib is not None:
             return _lib
-        if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_HERE, "_marshal.so"))):
-            raise RuntimeError(f"{LIB_PATH} or _marshal.so beside it is missing: build it with __graft_entry__.build() "
-                               "or python sparse_gemm_linears_amd/build.py")
+        _require(LIB_PATH)
         lib = ctypes.CDLL(LIB_PATH)
         P, I, F, B = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
         sig = {
@@ -422,6 +427,7 @@ def _marshal_module():
     global _marshal
     if _marshal is None:
         load_library()
+        _require(os.path.join(_HERE, "_marshal.so"))
         from . import _marshal as module
         module.set_status_check(_check)
         _marshal = module

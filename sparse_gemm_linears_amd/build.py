@@ -76,14 +76,13 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
         marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(_compile, SOURCES))
-        marshal = marshal.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_marshal(marshal)
+    _link_marshal(marshal.result())  # last: the library alone serves the FP8 linears
     if verbose:
         print("built", LIB, "and", MARSHAL)
     return LIB
