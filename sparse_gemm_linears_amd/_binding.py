@@ -151,12 +151,12 @@ def _codes(t: torch.Tensor) -> torch.Tensor:
 
 
 def _out(out, name, shape, dtype, like):
-    if out is None:  # contiguous; the _like and _strided forms cost 0.5 us less than torch.empty
+    if out is None:  # torch.empty's layout; the _like and _strided forms cost 0.5 us less
         if like.shape == shape:
-            return torch.empty_like(like, dtype=dtype)
+            return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
         strides = [1] * len(shape)
         for i in range(len(shape) - 1, 0, -1):
-            strides[i - 1] = strides[i] * shape[i]
+            strides[i - 1] = strides[i] * max(shape[i], 1)
         return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
     _want(out, name, dtype, shape)
     return out
