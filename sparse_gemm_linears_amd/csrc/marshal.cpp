@@ -38,13 +38,14 @@ std::string text_of(at::IntArrayRef s) {
 
 bool given(PyObject *o) { return o != Py_None; }
 
-// The tensor in o: of this type, on the GPU, contiguous and (unless sizes is
-// empty) of these sizes.  float8 tensors stand for bytes where `bytes` is set.
-const Tensor &want(PyObject *o, const char *name, at::ScalarType type, Sizes sizes = {}, bool bytes = false) {
+// The tensor in o: of this type (or of `bytes`, the float8 type that the bytes stand
+// for), on the GPU, contiguous and (unless sizes is empty) of these sizes.
+const Tensor &want(PyObject *o, const char *name, at::ScalarType type, Sizes sizes = {},
+                   at::ScalarType bytes = at::ScalarType::Undefined) {
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, std::string(name) + ": expected a torch.Tensor");
   const Tensor &t = THPVariable_Unpack(o);
   const at::ScalarType got = t.scalar_type();
-  if (got != type && !(bytes && (got == at::kFloat8_e4m3fn || got == at::kFloat8_e8m0fnu)))
+  if (got != type && (bytes == at::ScalarType::Undefined || got != bytes))
     raise(PyExc_TypeError,
           std::string(name) + ": expected dtype " + c10::toString(type) + ", got " + c10::toString(got));
   if (!t.is_cuda()) raise(PyExc_ValueError, std::string(name) + ": expected a device tensor");
@@ -58,7 +59,8 @@ const Tensor &want(PyObject *o, const char *name, at::ScalarType type, Sizes siz
 }
 
 // want() for a tensor of `dims` dimensions.
-const Tensor &want_dims(PyObject *o, const char *name, at::ScalarType type, int64_t dims, bool bytes = false) {
+const Tensor &want_dims(PyObject *o, const char *name, at::ScalarType type, int64_t dims,
+                        at::ScalarType bytes = at::ScalarType::Undefined) {
   const Tensor &t = want(o, name, type, {}, bytes);
   if (t.dim() != dims)
     raise(PyExc_ValueError,
@@ -68,7 +70,8 @@ const Tensor &want_dims(PyObject *o, const char *name, at::ScalarType type, int6
 
 // An output: the caller's tensor, or a new one beside `like` (the allocator's own
 // call: 0.3 us less for each tensor than at::empty with its dispatch).
-Tensor output(PyObject *o, const char *name, at::ScalarType type, Sizes sizes, const Tensor &like, bool bytes = false) {
+Tensor output(PyObject *o, const char *name, at::ScalarType type, Sizes sizes, const Tensor &like,
+              at::ScalarType bytes = at::ScalarType::Undefined) {
   if (given(o)) return want(o, name, type, sizes, bytes);
   return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
@@ -163,8 +166,9 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (keep_y) y = output(a[8], "y", at::kBFloat16, {M, K}, x);
     if (quantize) {
-      q = output(a[9], "q", at::kByte, {M, K}, x, true);
-      s = output(a[10], "scales", ue8m0 ? at::kByte : at::kFloat, {M, K / 128}, x, ue8m0);
+      q = output(a[9], "q", at::kByte, {M, K}, x, at::kFloat8_e4m3fn);
+      s = ue8m0 ? output(a[10], "scales", at::kByte, {M, K / 128}, x, at::kFloat8_e8m0fnu)
+                : output(a[10], "scales", at::kFloat, {M, K / 128}, x);
     }
     const float eps = (float)real(a[4]);
     hipStream_t stream = stream_of(a[11]);
@@ -194,12 +198,13 @@ struct Cache {
 Cache want_cache(PyObject *const *a, bool fp8) {
   Cache c;
   const at::ScalarType type = fp8 ? at::kByte : at::kBFloat16;
-  c.k = want_dims(a[0], "k_cache", type, 4, fp8);
+  const at::ScalarType bytes = fp8 ? at::kFloat8_e4m3fn : at::ScalarType::Undefined;
+  c.k = want_dims(a[0], "k_cache", type, 4, bytes);
   c.pages = c.k.size(0);
   c.heads = c.k.size(1);
   c.page = c.k.size(2);
   c.dim = c.k.size(3);
-  c.v = want(a[1], "v_cache", type, {c.pages, c.heads, c.page, c.dim}, fp8);
+  c.v = want(a[1], "v_cache", type, {c.pages, c.heads, c.page, c.dim}, bytes);
   if (fp8) {
     c.ks = want(a[2], "k_scale", at::kFloat, {c.pages, c.heads, c.page});
     c.vs = want(a[3], "v_scale", at::kFloat, {c.pages, c.heads, c.page});
