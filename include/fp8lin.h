@@ -427,7 +427,8 @@ fp8l_status fp8_add_rmsnorm_ue8m0(const uint16_t *x, const uint16_t *res, const 
  * other values and the value heads are copied.  Each result is rounded once: to
  * bf16, or for the _fp8 call to codes with a scale for each token and head.
  * Two tokens of one call must not have the same slot (which one stays is
- * unspecified).  With rot == 0 positions and cos_sin are not read (may be NULL).
+ * unspecified).  With rot == 0 positions and cos_sin are not read (may be NULL, and
+ * max_pos may be 0).
  */
 fp8l_status kv_rope_append(const uint16_t *qkv, const int32_t *positions, const int64_t *slots, const float *cos_sin,
                            int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved,

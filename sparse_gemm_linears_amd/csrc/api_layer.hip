@@ -46,7 +46,7 @@ bool bad_cache(int64_t Hq, int64_t Hkv, int64_t D, int64_t pages, int64_t page_s
 fp8l_status rope_append(AppendArgs a, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int64_t max_pos,
                         int64_t pages, int64_t page_size, bool fp8, hipStream_t stream) {
   if (bad_cache(Hq, Hkv, D, pages, page_size) || T < 0 || T > kMaxDim || T * (Hq + 2 * Hkv) * D > kMaxElems ||
-      rot < 0 || rot > D || rot % 16 != 0 || max_pos <= 0 || max_pos > kMaxDim)
+      rot < 0 || rot > D || rot % 16 != 0 || max_pos < (rot > 0) || max_pos > kMaxDim)
     return FP8L_ERR_SHAPE;
   if (T == 0) return FP8L_OK;
   if (!a.qkv || !a.slots || !a.q_out || !a.k_cache || !a.v_cache || (rot > 0 && (!a.positions || !a.cos_sin)) ||
