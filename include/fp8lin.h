@@ -58,7 +58,8 @@
  *                    (and M > 64 for the two *_linear calls);
  *                    for fp8_block_gemm_swiglu I plays the part of N;
  *                    the decoder-layer calls state their own limits;
- *   FP8L_ERR_ALIGN   a pointer is not 16-byte aligned;
+ *   FP8L_ERR_ALIGN   a pointer is not 16-byte aligned (arrays of the
+ *                    decoder-layer calls that need less state it);
  *   FP8L_ERR_ALIAS   an output overlaps an input or another output;
  *   FP8L_ERR_DEVICE  the current HIP device is missing or is not gfx950;
  *   FP8L_ERR_LAUNCH  the kernel launch was rejected by the runtime;
@@ -385,8 +386,9 @@ fp8l_status fp8_sparse24_linear(const uint16_t *x, const uint8_t *wvals, const u
  * p * page_size + off.  bf16 values, or (the _fp8 calls) e4m3 codes with one
  * fp32 scale amax / 448 for each token and head in k_scale and v_scale
  * [pages, Hkv, page_size].
- *   1 <= Hq, Hkv <= 1024; D is 64, 128 or 256; page_size a multiple of 16 up to
- *   65536; pages * page_size < 2^31; pages * page_size * Hkv * D <= 2^40.
+ *   1 <= Hq, Hkv <= 1024; D is 64, 128 or 256; page_size a multiple of 16 from 16 to
+ *   65536; pages >= 1; pages * page_size < 2^31; pages * page_size * Hkv * D <= 2^40.
+ * Numbers outside these and the limits stated with each call are FP8L_ERR_SHAPE.
  */
 
 /*
@@ -403,7 +405,8 @@ fp8l_status fp8_sparse24_linear(const uint16_t *x, const uint8_t *wvals, const u
  * The _ue8m0 call gives UE8M0 scale bytes as fp8_quant_act_ue8m0 does.  A group
  * with an infinity or a NaN gets a non-finite scale (UE8M0: the NaN byte 0xFF).
  * FP8L_ERR_NULL when exactly one of res and h, or of q and s, is NULL, or both
- * y and q are; FP8L_ERR_SHAPE for an eps out of range.
+ * y and q are; FP8L_ERR_SHAPE for an eps out of range.  0 <= M <= 2^24; K a
+ * multiple of 128, 128 .. 2^24; M * K <= 2^36.
  */
 fp8l_status fp8_add_rmsnorm(const uint16_t *x, const uint16_t *res, const uint16_t *w, float eps, int64_t M,
                             int64_t K, uint16_t *h, uint16_t *y, uint8_t *q, float *s, hipStream_t stream);
@@ -416,9 +419,10 @@ fp8l_status fp8_add_rmsnorm_ue8m0(const uint16_t *x, const uint16_t *res, const 
  *
  *   qkv [T, (Hq + 2 Hkv) D] bf16   a row holds the query heads, the key heads,
  *                                  the value heads (the y of fp8_block_gemm)
- *   positions [T] int32            clamped to 0 .. max_pos - 1
+ *   positions [T] int32            clamped to 0 .. max_pos - 1; 4-byte aligned
  *   slots [T] int64                the token's cache line; negative or past the
- *                                  cache: the token is not stored (padding)
+ *                                  cache: the token is not stored (padding);
+ *                                  8-byte aligned
  *   cos_sin [max_pos, rot] fp32    row p: rot / 2 cosines, then rot / 2 sines
  *   q_out [T, Hq, D] bf16          rotated queries (of every token)
  * The first rot values (a multiple of 16, 0 .. D) of each query and key head
@@ -428,7 +432,7 @@ fp8l_status fp8_add_rmsnorm_ue8m0(const uint16_t *x, const uint16_t *res, const 
  * bf16, or for the _fp8 call to codes with a scale for each token and head.
  * Two tokens of one call must not have the same slot (which one stays is
  * unspecified).  With rot == 0 positions and cos_sin are not read (may be NULL, and
- * max_pos may be 0).
+ * max_pos may be 0).  0 <= T <= 2^24; T (Hq + 2 Hkv) D <= 2^36; 1 <= max_pos <= 2^24.
  */
 fp8l_status kv_rope_append(const uint16_t *qkv, const int32_t *positions, const int64_t *slots, const float *cos_sin,
                            int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved,
@@ -446,21 +450,24 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  *   q [B,Hq,D] bf16                  Hq a multiple of Hkv: query head n reads
  *                                    key head n / (Hq / Hkv)
  *   block_table [B,max_pages] int32  page of tokens i page_size .. of sequence b
- *                                    at [b,i]; entries past its length are not used
+ *                                    at [b,i]; entries past its length are not
+ *                                    used; max_pages >= 1; 4-byte aligned
  *   seq_lens [B] int32               tokens in the cache, the new one included;
- *                                    clamped to 0 .. max_len
+ *                                    clamped to 0 .. max_len; 4-byte aligned
  *   max_len                          a bound on seq_lens known to the host,
  *                                    0 .. max_pages * page_size (<= 2^30)
  *   scale, softcap, window           score = scale (q . k); with softcap > 0,
  *                                    softcap tanh(score / softcap); with window >
- *                                    0 only the last `window` tokens count
+ *                                    0 only the last `window` tokens count;
+ *                                    scale finite, 0 <= softcap < inf, window >= 0
  *   o [B,Hq,D] bf16                  sum_t softmax(score)_t v_t
- *   lse [B,Hq] fp32 or NULL          log sum_t exp(score_t), natural logarithm
+ *   lse [B,Hq] fp32 or NULL          log sum_t exp(score_t), natural logarithm;
+ *                                    4-byte aligned
  * A sequence of length 0, or whose scores are all -inf, gives o = 0 and lse =
  * -inf.  Scores, softmax sums and
  * o are held in fp32; the softmax weights enter the product with v as two bf16
- * numbers each (17 bits).  Cache lines past a sequence's length or before its
- * window may hold anything.  Page numbers out of range are clamped: such rows
+ * numbers each (17 bits), so that an infinite value of a token that counts gives NaN.
+ * Cache lines past a sequence's length or before its window may hold anything.  Page numbers out of range are clamped: such rows
  * are unspecified, with no access outside the cache.  Beyond short sequences rows
  * are divided, or a ragged batch's tokens are divided evenly over the device,
  * with fp32 partials in library scratch memory that a second kernel joins in a

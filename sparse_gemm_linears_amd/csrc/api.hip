@@ -303,7 +303,7 @@ const char *fp8lin_status_str(fp8l_status status) {
     case FP8L_ERR_SHAPE:
       return "unsupported shape (K and N must be positive multiples of 128, M >= 0, each <= 2^24; M <= 64 for the "
              "*_linear calls; for the decoder-layer calls see the limits stated with them)";
-    case FP8L_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+    case FP8L_ERR_ALIGN: return "a pointer is not 16-byte aligned (or as stated with the call)";
     case FP8L_ERR_ALIAS: return "an output overlaps an input or another output";
     case FP8L_ERR_DEVICE: return "no gfx950 (MI355X) device is current";
     case FP8L_ERR_LAUNCH: return "kernel launch failed";
