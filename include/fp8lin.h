@@ -466,7 +466,8 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  * A sequence of length 0, or whose scores are all -inf, gives o = 0 and lse =
  * -inf.  Scores, softmax sums and
  * o are held in fp32; the softmax weights enter the product with v as two bf16
- * numbers each (17 bits), so that an infinite value of a token that counts gives NaN.
+ * numbers each (17 bits), so that an infinite value of a token that counts gives an
+ * infinity or NaN in its place of the row's heads, by how their weights round.
  * Cache lines past a sequence's length or before its window may hold anything.  Page numbers out of range are clamped: such rows
  * are unspecified, with no access outside the cache.  Beyond short sequences rows
  * are divided, or a ragged batch's tokens are divided evenly over the device,

@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
 from decode_forms import BATCHES
 from test_layer_gpu import attend_case
@@ -27,3 +28,22 @@ def test_forms(gpu_lib, batch, fp8):
     with and without a window, and short rows in workgroups of one, two and four waves."""
     attend_case(gpu_lib, batch.lens(), batch.Hq, batch.Hkv, batch.D, batch.page, fp8, window=batch.window,
                 max_len=batch.max_len)
+
+
+@pytest.mark.parametrize("lens,max_len", [([7], 32), ([40, 3], 4096), ([900] * 40, 4096)])
+def test_infinite_values_stay_in_their_place(gpu_lib, lens, max_len):
+    """An infinite value of a token that counts: an infinity or NaN in its own place of the row's heads, and nothing
+    else moves."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    B, hq, hkv, d, page = len(lens), 8, 2, 128, 16
+    per = max_len // page
+    k, v = (torch.randn(B * per, hkv, page, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(B, hq, d, generator=g, device="cuda").bfloat16()
+    pages = torch.arange(B * per, dtype=torch.int32, device="cuda").view(B, per)
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = gpu_lib.paged_decode_attention(q, k, v, pages, seq)
+    v[0, 1, 2, 77] = float("inf")  # token 2 of the first sequence, its second key head
+    got = gpu_lib.paged_decode_attention(q, k, v, pages, seq)
+    assert not torch.isfinite(got[0, 4:, 77]).any()
+    got[0, 4:, 77] = want[0, 4:, 77]
+    assert torch.equal(got, want)
