@@ -1,5 +1,7 @@
 // How the attention of paged_decode.hip divides a batch: the launch plan, which the
 // host makes from sizes alone, and the layouts that the plan and the kernels share.
+// Times are of one call of a replayed graph over three sets of inputs in turn, or of the
+// kernel alone in a trace where that is said.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -22,8 +24,8 @@ __host__ __device__ inline int first_token(int len, int window) {
 // rows of a sequence follow each other (bands of query heads within a key head),
 // and wave i of 2^log2_parts takes units share_start(i) .. share_start(i + 1) - 1 of
 // all.  A unit is a tile, and one more for the end of each row, which costs about as
-// much (shares of equal tiles took 77 us on 64 sequences of 1 to 8192 tokens where
-// sequences of equal length took 63).
+// much (shares of equal tiles took the kernel 77 us on 64 sequences of 1 to 8192 tokens
+// where sequences of equal length took 63).
 struct DecodePlan {
   int row_waves, splits;
   int first_row;  // of a launch (splits == 1)

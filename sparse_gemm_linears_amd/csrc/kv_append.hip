@@ -5,8 +5,10 @@
 // once: to bf16, or for an e4m3 cache to codes with one fp32 scale
 // amax / 448 for each token and head.  HBM-bound for many tokens (each value
 // is read once and written once): 8192 tokens of 48 heads of 128 into an e4m3
-// cache, 189 MB in 37.5 us, 5.0 TB/s.  One token is bound by two memory
-// latencies and the launch: 2.4 us.
+// cache, 189 MB in 33.8 us, 5.6 TB/s.  One token is bound by two memory
+// latencies and the launch: 3.0 us.  (Times in this file: one call of a replayed graph of
+// twelve over three sets of inputs in turn.  Issued one by one, calls take 37.5 and
+// 5.3 us.)
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "launch_layer.hpp"
@@ -122,9 +124,11 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_lo
 // the workgroups fewer and their loops longer, so a number is taken if it needs a
 // fifth fewer lane steps than the last one taken, loops of five at most, and leaves
 // two workgroups for each compute unit.  With 1, 2, 4, 8, 16 tokens (* the choice): 12603
-// tokens of 34 heads of 64 (e4m3 cache) 22.0 20.1 19.4* 19.4 22.7 us, 9000 of 56 (bf16)
-// 26.6* 26.1 27.9 30.1 33.2, 30000 of 10 34.0 23.6 16.1 14.7 14.5*; of 128, 8192 of 48
-// 35.4 33.9* 36.4 36.2 37.0, 1100 of 48 7.2 7.1* 8.6 12.4 20.9, 600 of 48 5.3* 5.7 7.4 11.6.
+// tokens of 34 heads of 64 (e4m3 cache) 23.3 20.9 19.8* 20.0 23.4 us, 9000 of 56 (bf16)
+// 26.0* 25.9 27.8 29.2 33.1, 30000 of 10 34.1 23.6 16.1 14.6 14.5*; of 128, 8192 of 48
+// 35.2 33.8* 36.5 36.5 37.7, 1100 of 48 7.2 7.2* 8.6 12.4 20.9, 600 of 48 5.4* 5.7 7.2 11.7.
+// It gives away a few percent where the next number's saving is just under a fifth: 6000 of
+// 18 of 128 (bf16) 12.5 12.6 11.3* 10.6 13.4, 8000 of 10 of 256 16.2 15.3 15.0* 14.6 15.0.
 int tokens_log2(const AppendArgs &a, int cus) {
   const int heads = a.Hq + 2 * a.Hkv, sets = 256 / (a.D / 16);
   int best = 0;

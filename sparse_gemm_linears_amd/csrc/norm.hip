@@ -5,8 +5,10 @@
 // One pass over HBM: a row is held in fp32 registers between the sum of
 // squares and the output, so x and res are read once and h, the codes and the
 // scales written once (7.03 bytes per element with a residual).  HBM-bound
-// for many rows: 8192 x 7168 with a residual, 413 MB in 74 us, 5.6 TB/s.  One row
-// is bound by two memory latencies and the launch: 1 x 4096 in 2.4 us.
+// for many rows: 8192 x 7168 with a residual, 413 MB in 66 us, 6.3 TB/s.  One row
+// is bound by two memory latencies and the launch: 1 x 4096 in 2.9 us.  (Times in this
+// file: one call of a replayed graph of twelve over three sets of inputs in turn.  Issued
+// one by one, calls take 75 and 7 us.)
 //
 // Numbers: h is exact in fp32 up to one rounding; the sum of squares is taken
 // in fp32 over the unrounded h, each lane's elements in order and the lanes in
@@ -192,9 +194,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a, ScaleKin
 }
 
 // Inputs that the caches cannot hold (256 MB for all of a launch's data) are read
-// past them: 8192 x 7168 with a residual 76.1 -> 68.2 us, 16384 x 3584 73.0 -> 65.5.
+// past them: 8192 x 7168 with a residual 73.5 -> 65.8 us, 16384 x 3584 74.2 -> 65.7.
 // Smaller ones may be there from the call that made them: 2048 x 16384 with a
-// residual 41.5 -> 42.8 us, 4093 x 4096 without 15.7 -> 17.8 us so.
+// residual 41.2 -> 42.7 us, 4093 x 4096 without (bf16 output too) 15.8 -> 17.8 us so.
 constexpr int64_t kStreamBytes = int64_t(192) << 20;
 bool streams(const NormArgs &a) { return a.M * a.K * (a.res ? 4 : 2) > kStreamBytes; }
 

@@ -23,9 +23,10 @@
 // sequences, one sequence alone, windows, and batches that give each wave a few tiles
 // at most are divided by the grid, without the search (row_kernel).
 //
-// Measured with 8 key heads of 128: 131072 tokens of one sequence in bf16, 537 MB in
-// 84 us, 6.4 TB/s, and 5 us for the join; 64 sequences of 1 to 8192 tokens in e4m3,
-// 373 MB in 68 us, 5.5 TB/s, and 6 us; 777 tokens of one sequence 5.7 us and 4 us.
+// Measured with 8 key heads of 128 (medians of a kernel trace): 131072 tokens of one
+// sequence in bf16, 537 MB in 84 us, 6.4 TB/s, and 5 us for the join; 64 sequences of 1
+// to 8192 tokens in e4m3, 373 MB in 68 us, 5.5 TB/s, and 6 us; 777 tokens of one sequence
+// 5.7 us and 4 us.
 //
 // Layouts (v_mfma_f32_16x16x32_bf16: lane l, n = l % 16, g = l / 16):
 //   scores   A = K: row n is token n of a half tile, B = Q: column n is a query
