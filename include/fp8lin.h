@@ -404,6 +404,8 @@ fp8l_status fp8_sparse24_linear(const uint16_t *x, const uint8_t *wvals, const u
  *                    448), q = enc(fp32(v / s)); both NULL: not produced
  * The _ue8m0 call gives UE8M0 scale bytes as fp8_quant_act_ue8m0 does.  A group
  * with an infinity or a NaN gets a non-finite scale (UE8M0: the NaN byte 0xFF).
+ * The squares are summed in fp32 too: where the sum passes its range (|x + res|
+ * from about 2^64 / sqrt K on) the row's finite values become 0.
  * FP8L_ERR_NULL when exactly one of res and h, or of q and s, is NULL, or both
  * y and q are; FP8L_ERR_SHAPE for an eps out of range.  0 <= M <= 2^24; K a
  * multiple of 128, 128 .. 2^24; M * K <= 2^36.
@@ -467,7 +469,9 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  * -inf.  Scores, softmax sums and
  * o are held in fp32; the softmax weights enter the product with v as two bf16
  * numbers each (17 bits), so that an infinite value of a token that counts gives an
- * infinity or NaN in its place of the row's heads, by how their weights round.
+ * infinity or NaN in its place of the row's heads, by how their weights round.  Sums
+ * are divided at the end, and may pass fp32's range where the largest |v| times the
+ * tokens that count reaches 2^120.
  * Cache lines past a sequence's length or before its window may hold anything.  Page numbers out of range are clamped: such rows
  * are unspecified, with no access outside the cache.  Beyond short sequences rows
  * are divided, or a ragged batch's tokens are divided evenly over the device,

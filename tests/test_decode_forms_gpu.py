@@ -47,3 +47,21 @@ def test_infinite_values_stay_in_their_place(gpu_lib, lens, max_len):
     assert not torch.isfinite(got[0, 4:, 77]).any()
     got[0, 4:, 77] = want[0, 4:, 77]
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("lens,max_len", [([9], 32), ([700, 3, 0], 4096), ([900] * 40, 4096)])
+def test_values_of_any_size(gpu_lib, lens, max_len):
+    """Values times a power of two give outputs times it, bit for bit, within the stated range and down to where the
+    weights' second parts stay normal."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    B, hq, hkv, d, page = len(lens), 6, 2, 64, 16
+    per = max_len // page
+    k, v = (torch.randn(B * per, hkv, page, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    v = torch.where(v.abs() < 2.0 ** -6, torch.full_like(v, 0.25), v)
+    q = torch.randn(B, hq, d, generator=g, device="cuda").bfloat16()
+    pages = torch.arange(B * per, dtype=torch.int32, device="cuda").view(B, per)
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want, lse = gpu_lib.paged_decode_attention(q, k, v, pages, seq, return_lse=True)
+    for power in (2.0 ** 105, 2.0 ** -40):  # below 8 x 2^105 x 900 tokens < 2^120
+        got, again = gpu_lib.paged_decode_attention(q, k, v * power, pages, seq, return_lse=True)
+        assert torch.isfinite(got).all() and torch.equal(got, want * power) and torch.equal(again, lse)
