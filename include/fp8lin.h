@@ -447,6 +447,33 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
                                hipStream_t stream);
 
 /*
+ * kv_rope_append with a root-mean-square norm of each query and key head before
+ * the rotation, and the turned keys in bf16 on request (for the attention of a
+ * prompt over its own keys, prompt_attention).
+ *
+ *   q_weight, k_weight [D] bf16    v_d = x_d / sqrt(mean_d x_d^2 + eps) * w_d in fp32, over
+ *                                  the whole head; NULL: those heads are not normed.
+ *                                  0 <= eps < inf.  The squares are summed in fp32:
+ *                                  where their sum passes its range the head's
+ *                                  finite values become 0
+ *   k_out [T, Hkv, D] bf16         keys of every token after norm and rotation, or
+ *                                  NULL
+ * Everything else, the limits included, is as in kv_rope_append; norm and rotation
+ * are in fp32 and each result is rounded once.
+ */
+fp8l_status kv_norm_rope_append(const uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                                const int32_t *positions, const int64_t *slots, const float *cos_sin, int64_t T,
+                                int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved, int64_t max_pos,
+                                int64_t pages, int64_t page_size, uint16_t *q_out, uint16_t *k_out, uint16_t *k_cache,
+                                uint16_t *v_cache, hipStream_t stream);
+fp8l_status kv_norm_rope_append_fp8(const uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                                    const int32_t *positions, const int64_t *slots, const float *cos_sin, int64_t T,
+                                    int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved, int64_t max_pos,
+                                    int64_t pages, int64_t page_size, uint16_t *q_out, uint16_t *k_out,
+                                    uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+                                    hipStream_t stream);
+
+/*
  * Attention of one new token of each of B sequences over the paged cache.
  *
  *   q [B,Hq,D] bf16                  Hq a multiple of Hkv: query head n reads

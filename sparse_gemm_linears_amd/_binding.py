@@ -38,7 +38,7 @@ EXPORTS = ("fp8_quant_act", "fp8_quant_weight_block", "prune24_compress", "fp8_b
            "fp8_grouped_gemm", "fp8_block_gemm_swiglu", "fp8_block_linear", "fp8_sparse24_linear",
            "fp8_quant_act_tensor", "fp8_quant_act_static", "fp8_quant_weight_tensor", "prune24_compress_tensor",
            "fp8_block_gemm_noalloc", "fp8_add_rmsnorm", "fp8_add_rmsnorm_ue8m0", "kv_rope_append",
-           "kv_rope_append_fp8", "paged_decode_attention", "paged_decode_attention_fp8",
+           "kv_rope_append_fp8", "kv_norm_rope_append", "kv_norm_rope_append_fp8", "paged_decode_attention", "paged_decode_attention_fp8",
            "fp8lin_release_graph_scratch", "fp8lin_status_str")
 MAX_LINEAR_M = 64  # the fused-quantization calls take decode-sized batches
 
@@ -93,6 +93,8 @@ def load_library():
             "fp8_add_rmsnorm_ue8m0": [P, P, P, F, I, I, P, P, P, P, P],
             "kv_rope_append": [P, P, P, P, I, I, I, I, I, B, I, I, I, P, P, P, P],
             "kv_rope_append_fp8": [P, P, P, P, I, I, I, I, I, B, I, I, I, P, P, P, P, P, P],
+            "kv_norm_rope_append": [P, P, P, F, P, P, P, I, I, I, I, I, B, I, I, I, P, P, P, P, P],
+            "kv_norm_rope_append_fp8": [P, P, P, F, P, P, P, I, I, I, I, I, B, I, I, I, P, P, P, P, P, P, P],
             "paged_decode_attention": [P, P, P, P, P, I, I, I, I, I, I, I, I, F, F, I, P, P, P],
             "paged_decode_attention_fp8": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, F, I, P, P, P],
         }
@@ -465,6 +467,24 @@ def kv_rope_append_fp8(qkv, positions, slots, cos_sin, k_cache, v_cache, k_scale
     """kv_rope_append into an e4m3 cache: codes [pages,Hkv,page,D] and fp32 scales [pages,Hkv,page]."""
     return _marshal_module().rope_append(True, qkv, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale,
                                          interleaved, q, _stream_of(qkv))
+
+
+def kv_norm_rope_append(qkv, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, eps: float = 1e-6,
+                        interleaved: bool = False, return_keys: bool = False, q=None, k=None):
+    """kv_rope_append with root-mean-square norms of the query and key heads before the rotation: q_weight and k_weight
+    [D] bf16 (None: those heads are not normed).  With ``return_keys`` the result is (queries, keys [T,Hkv,D] bf16),
+    the keys of every token after norm and rotation (for prompt_attention)."""
+    return _marshal_module().norm_rope_append(False, qkv, q_weight, k_weight, positions, slots, cos_sin, k_cache,
+                                              v_cache, None, None, eps, interleaved, return_keys, q, k,
+                                              _stream_of(qkv))
+
+
+def kv_norm_rope_append_fp8(qkv, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale,
+                            eps: float = 1e-6, interleaved: bool = False, return_keys: bool = False, q=None, k=None):
+    """kv_norm_rope_append into an e4m3 cache: codes [pages,Hkv,page,D] and fp32 scales [pages,Hkv,page]."""
+    return _marshal_module().norm_rope_append(True, qkv, q_weight, k_weight, positions, slots, cos_sin, k_cache,
+                                              v_cache, k_scale, v_scale, eps, interleaved, return_keys, q, k,
+                                              _stream_of(qkv))
 
 
 def paged_decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0,

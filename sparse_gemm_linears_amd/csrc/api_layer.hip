@@ -46,13 +46,15 @@ bool bad_cache(int64_t Hq, int64_t Hkv, int64_t D, int64_t pages, int64_t page_s
 fp8l_status rope_append(AppendArgs a, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int64_t max_pos,
                         int64_t pages, int64_t page_size, bool fp8, hipStream_t stream) {
   if (bad_cache(Hq, Hkv, D, pages, page_size) || T < 0 || T > kMaxDim || T * (Hq + 2 * Hkv) * D > kMaxElems ||
-      rot < 0 || rot > D || rot % 16 != 0 || max_pos < (rot > 0) || max_pos > kMaxDim)
+      rot < 0 || rot > D || rot % 16 != 0 || max_pos < (rot > 0) || max_pos > kMaxDim || !(a.eps >= 0.0f) ||
+      std::isinf(a.eps))
     return FP8L_ERR_SHAPE;
   if (T == 0) return FP8L_OK;
   if (!a.qkv || !a.slots || !a.q_out || !a.k_cache || !a.v_cache || (rot > 0 && (!a.positions || !a.cos_sin)) ||
       (fp8 && (!a.k_scale || !a.v_scale)))
     return FP8L_ERR_NULL;
-  const void *ptrs[] = {a.qkv, a.cos_sin, a.q_out, a.k_cache, a.v_cache, a.k_scale, a.v_scale};
+  const void *ptrs[] = {a.qkv,     a.cos_sin, a.q_out,   a.k_cache,  a.v_cache,
+                        a.k_scale, a.v_scale, a.k_out,   a.q_weight, a.k_weight};
   for (const void *p : ptrs)
     if (!aligned16(p)) return FP8L_ERR_ALIGN;
   if (((uintptr_t)a.positions & 3u) || ((uintptr_t)a.slots & 7u)) return FP8L_ERR_ALIGN;
@@ -60,13 +62,16 @@ fp8l_status rope_append(AppendArgs a, int64_t T, int64_t Hq, int64_t Hkv, int64_
   const Range ins[] = {{a.qkv, T * (Hq + 2 * Hkv) * D * 2},
                        {a.positions, rot > 0 ? T * 4 : 0},
                        {a.slots, T * 8},
-                       {a.cos_sin, max_pos * rot * 4}};
+                       {a.cos_sin, max_pos * rot * 4},
+                       {a.q_weight, a.q_weight ? D * 2 : 0},
+                       {a.k_weight, a.k_weight ? D * 2 : 0}};
   const Range outs[] = {{a.q_out, T * Hq * D * 2},
+                        {a.k_out, a.k_out ? T * Hkv * D * 2 : 0},
                         {a.k_cache, cache_bytes},
                         {a.v_cache, cache_bytes},
                         {a.k_scale, fp8 ? lines * 4 : 0},
                         {a.v_scale, fp8 ? lines * 4 : 0}};
-  if (any_alias(outs, 5, ins, 4)) return FP8L_ERR_ALIAS;
+  if (any_alias(outs, 6, ins, 6)) return FP8L_ERR_ALIAS;
   if (fp8l_status st = check_device()) return st;
   a.T = T;
   a.Hq = (int)Hq;
@@ -166,6 +171,51 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
   a.cos_sin = cos_sin;
   a.interleaved = interleaved != 0;
   a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return rope_append(a, T, Hq, Hkv, D, rot, max_pos, pages, page_size, true, stream);
+}
+
+fp8l_status kv_norm_rope_append(const uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                                const int32_t *positions, const int64_t *slots, const float *cos_sin, int64_t T,
+                                int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved, int64_t max_pos,
+                                int64_t pages, int64_t page_size, uint16_t *q_out, uint16_t *k_out, uint16_t *k_cache,
+                                uint16_t *v_cache, hipStream_t stream) {
+  AppendArgs a{};
+  a.qkv = qkv;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.slots = slots;
+  a.cos_sin = cos_sin;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  return rope_append(a, T, Hq, Hkv, D, rot, max_pos, pages, page_size, false, stream);
+}
+
+fp8l_status kv_norm_rope_append_fp8(const uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                                    const int32_t *positions, const int64_t *slots, const float *cos_sin, int64_t T,
+                                    int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int interleaved, int64_t max_pos,
+                                    int64_t pages, int64_t page_size, uint16_t *q_out, uint16_t *k_out,
+                                    uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+                                    hipStream_t stream) {
+  AppendArgs a{};
+  a.qkv = qkv;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.slots = slots;
+  a.cos_sin = cos_sin;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out;
+  a.k_out = k_out;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.k_scale = k_scale;

@@ -1,5 +1,6 @@
 // Rotary position embedding of the query and key heads of a QKV projection and
-// the append of the keys and values to a paged cache.
+// the append of the keys and values to a paged cache; before the rotation, on
+// request, the root-mean-square norm of each query and key head.
 //
 // A rotated pair (a, b) becomes (a cos - b sin, b cos + a sin), in fp32, rounded
 // once: to bf16, or for an e4m3 cache to codes with one fp32 scale
@@ -9,6 +10,8 @@
 // latencies and the launch: 3.0 us.  (Times in this file: one call of a replayed graph of
 // twelve over three sets of inputs in turn.  Issued one by one, calls take 37.5 and
 // 5.3 us.)
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "launch_layer.hpp"
@@ -26,11 +29,51 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   return v;
 }
 
+// The pair (x, y) turned.  Which product is fused is written out, so that every form of
+// the kernel gives the same bits.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void turn(float x, float y, float c, float s, float &a, float &b) {
+  a = __builtin_fmaf(x, c, -(y * s));
+  b = NEIGHBOURS ? __builtin_fmaf(y, c, x * s) : __builtin_fmaf(x, s, y * c);
+}
+
+// Sum over aligned sets of L lanes (4, 8 or 16), in every lane of the set.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  auto from = [&](auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  v += from(std::integral_constant<int, 0xB1>());
+  v += from(std::integral_constant<int, 0x4E>());
+  if constexpr (L >= 8) v += from(std::integral_constant<int, 0x141>());
+  if constexpr (L >= 16) v += from(std::integral_constant<int, 0x140>());
+  return v;
+}
+
+// x / sqrt(mean x^2 + eps) * w of a head of D values, 16 in each of D / 16 lanes, in fp32
+// (an infinite mean leaves 0 of finite values, like the residual norm).
+template <int D>
+__device__ __forceinline__ void norm_head(float (&f0)[8], float (&f1)[8], const uint4 &w0, const uint4 &w1, float eps) {
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; j++) sum = __builtin_fmaf(f0[j], f0[j], __builtin_fmaf(f1[j], f1[j], sum));
+  const float r = 1.0f / sqrtf(lanes_sum<D / 16>(sum) * (1.0f / D) + eps);
+  float g0[8], g1[8];
+  unpack8(w0, g0);
+  unpack8(w1, g1);
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    f0[j] = f0[j] * r * g0[j];
+    f1[j] = f1[j] * r * g1[j];
+  }
+}
+
 // D / 16 lanes hold one head: two chunks of eight values each, which are the
 // two halves of eight pairs where the lane rotates.  A workgroup covers 2^tokens_log2
 // tokens; a set of lanes keeps one token, with its angles in registers, and takes
-// its heads in strides of 256 16 / D >> tokens_log2.
-template <int D, bool FP8>
+// its heads in strides of 256 16 / D >> tokens_log2.  MORE: heads may be normed, and
+// the turned keys are stored in bf16 too where the caller wants them.
+template <int D, bool FP8, bool MORE>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_log2) {
   constexpr int L = D / 16;
   const int u = threadIdx.x % L, set = threadIdx.x / L;
@@ -58,6 +101,15 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_lo
     cs[0] = k0.x; cs[1] = k0.y; cs[2] = k0.z; cs[3] = k0.w; cs[4] = k1.x; cs[5] = k1.y; cs[6] = k1.z; cs[7] = k1.w;
     sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
   }
+  uint4 qw[2], kw[2];  // weights of the lane's columns
+  if constexpr (MORE) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int at = i ? c1 : c0;
+      qw[i] = a.q_weight ? *reinterpret_cast<const uint4 *>(a.q_weight + at) : make_uint4(0, 0, 0, 0);
+      kw[i] = a.k_weight ? *reinterpret_cast<const uint4 *>(a.k_weight + at) : make_uint4(0, 0, 0, 0);
+    }
+  }
   const bool stored = slot >= 0 && slot < (int64_t)a.n_slots;
   const uint32_t page = stored ? (uint32_t)slot / a.page_size : 0, off = stored ? (uint32_t)slot % a.page_size : 0;
   // turns, rounds and stores head h
@@ -65,22 +117,26 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_lo
     float f0[8], f1[8];
     unpack8(r[0], f0);
     unpack8(r[1], f1);
+    if constexpr (MORE) {
+      if (h < a.Hq) {
+        if (a.q_weight) norm_head<D>(f0, f1, qw[0], qw[1], a.eps);
+      } else if (h < a.Hq + a.Hkv) {
+        if (a.k_weight) norm_head<D>(f0, f1, kw[0], kw[1], a.eps);
+      }
+    }
     if (h < a.Hq + a.Hkv && u < turning) {
       if (a.interleaved) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           const float x0 = f0[2 * j], y0 = f0[2 * j + 1], x1 = f1[2 * j], y1 = f1[2 * j + 1];
-          f0[2 * j] = x0 * cs[j] - y0 * sn[j];
-          f0[2 * j + 1] = y0 * cs[j] + x0 * sn[j];
-          f1[2 * j] = x1 * cs[4 + j] - y1 * sn[4 + j];
-          f1[2 * j + 1] = y1 * cs[4 + j] + x1 * sn[4 + j];
+          turn<true>(x0, y0, cs[j], sn[j], f0[2 * j], f0[2 * j + 1]);
+          turn<true>(x1, y1, cs[4 + j], sn[4 + j], f1[2 * j], f1[2 * j + 1]);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
           const float x = f0[j], y = f1[j];
-          f0[j] = x * cs[j] - y * sn[j];
-          f1[j] = y * cs[j] + x * sn[j];
+          turn<false>(x, y, cs[j], sn[j], f0[j], f1[j]);
         }
       }
     }
@@ -92,6 +148,13 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int tokens_lo
     }
     const bool value = h >= a.Hq + a.Hkv;
     const int kvh = h - a.Hq - (value ? a.Hkv : 0);
+    if constexpr (MORE) {
+      if (a.k_out && !value) {
+        uint16_t *dst = a.k_out + (token * a.Hkv + kvh) * D;
+        *reinterpret_cast<uint4 *>(dst + c0) = pack8(f0);
+        *reinterpret_cast<uint4 *>(dst + c1) = pack8(f1);
+      }
+    }
     const int64_t line = ((int64_t)page * a.Hkv + kvh) * a.page_size + off;
     if constexpr (FP8) {
       uint32_t m = 0;
@@ -149,10 +212,15 @@ template <int D>
 void launch_append(const AppendArgs &a, hipStream_t stream) {
   const int lg = tokens_log2(a, device_cu_count());
   const dim3 grid((unsigned)((a.T + (1 << lg) - 1) >> lg)), block(256);
-  if (a.k_scale)
-    hipLaunchKernelGGL((append_kernel<D, true>), grid, block, 0, stream, a, lg);
+  const bool more = a.q_weight || a.k_weight || a.k_out;
+  if (a.k_scale && more)
+    hipLaunchKernelGGL((append_kernel<D, true, true>), grid, block, 0, stream, a, lg);
+  else if (a.k_scale)
+    hipLaunchKernelGGL((append_kernel<D, true, false>), grid, block, 0, stream, a, lg);
+  else if (more)
+    hipLaunchKernelGGL((append_kernel<D, false, true>), grid, block, 0, stream, a, lg);
   else
-    hipLaunchKernelGGL((append_kernel<D, false>), grid, block, 0, stream, a, lg);
+    hipLaunchKernelGGL((append_kernel<D, false, false>), grid, block, 0, stream, a, lg);
 }
 
 }  // namespace

@@ -24,6 +24,8 @@ hipError_t launch_add_rmsnorm(const NormArgs &a, ScaleKind kind, hipStream_t str
 
 struct AppendArgs {
   const uint16_t *qkv;
+  const uint16_t *q_weight, *k_weight;  // of the heads' norms; NULL: not normed
+  float eps;
   const int32_t *positions;
   const int64_t *slots;
   const float *cos_sin;
@@ -32,7 +34,7 @@ struct AppendArgs {
   bool interleaved;
   int max_pos;
   uint32_t n_slots, page_size;
-  uint16_t *q_out;
+  uint16_t *q_out, *k_out;    // k_out may be NULL
   void *k_cache, *v_cache;    // bf16, or e4m3 codes when the scales are given
   float *k_scale, *v_scale;   // both NULL for a bf16 cache
 };

@@ -128,6 +128,14 @@ PyObject *wrap_or_none(const Tensor &t) {
   Py_RETURN_NONE;
 }
 
+PyObject *pair(const Tensor &first, const Tensor &second) {
+  PyObject *out = PyTuple_New(2);
+  if (!out) throw Raised{};
+  PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(first));
+  PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(second));
+  return out;
+}
+
 // Runs f and turns C++ exceptions into Python's.
 template <class F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t expected, F f) {
@@ -246,6 +254,48 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// (fp8, qkv, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale, eps, interleaved,
+// return_keys, q, k, stream) -> q or (q, k)
+PyObject *norm_rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject * {
+    const bool fp8 = truth(a[0]), return_keys = truth(a[13]);
+    const Cache c = want_cache(a + 7, fp8);
+    const Tensor &qkv = want_dims(a[1], "qkv", at::kBFloat16, 2);
+    const int64_t T = qkv.size(0), width = qkv.size(1);
+    const int64_t Hq = c.dim > 0 ? width / c.dim - 2 * c.heads : 0;
+    if (Hq <= 0 || width % c.dim)
+      raise(PyExc_ValueError, "qkv: " + std::to_string(width) + " columns do not hold query heads beside 2 x " +
+                                  std::to_string(c.heads) + " heads of " + std::to_string(c.dim));
+    Tensor qw, kw, k;
+    if (given(a[2])) qw = want(a[2], "q_weight", at::kBFloat16, {c.dim});
+    if (given(a[3])) kw = want(a[3], "k_weight", at::kBFloat16, {c.dim});
+    const Tensor &positions = want(a[4], "positions", at::kInt, {T});
+    const Tensor &slots = want(a[5], "slots", at::kLong, {T});
+    const Tensor &table = want_dims(a[6], "cos_sin", at::kFloat, 2);
+    const float eps = (float)real(a[11]);
+    const int interleaved = truth(a[12]);
+    const Tensor q = output(a[14], "q", at::kBFloat16, {T, Hq, c.dim}, qkv);
+    if (return_keys || given(a[15])) k = output(a[15], "k", at::kBFloat16, {T, c.heads, c.dim}, qkv);
+    hipStream_t stream = stream_of(a[16]);
+    const int64_t max_pos = table.size(0), rot = table.size(1);
+    const auto *xp = data<uint16_t>(qkv), *qwp = data<uint16_t>(qw), *kwp = data<uint16_t>(kw);
+    const auto *pp = data<int32_t>(positions);
+    const auto *lp = data<int64_t>(slots);
+    const auto *tp = data<float>(table);
+    auto *qp = data<uint16_t>(q), *kp = data<uint16_t>(k);
+    check(fp8 ? "kv_norm_rope_append_fp8" : "kv_norm_rope_append", unlocked([&] {
+            return fp8 ? kv_norm_rope_append_fp8(xp, qwp, kwp, eps, pp, lp, tp, T, Hq, c.heads, c.dim, rot, interleaved,
+                                                 max_pos, c.pages, c.page, qp, kp, data<uint8_t>(c.k),
+                                                 data<uint8_t>(c.v), data<float>(c.ks), data<float>(c.vs), stream)
+                       : kv_norm_rope_append(xp, qwp, kwp, eps, pp, lp, tp, T, Hq, c.heads, c.dim, rot, interleaved,
+                                             max_pos, c.pages, c.page, qp, kp, data<uint16_t>(c.k),
+                                             data<uint16_t>(c.v), stream);
+          }));
+    if (!return_keys) return THPVariable_Wrap(q);
+    return pair(q, k);
+  });
+}
+
 // (fp8, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale, softcap, window, max_len, return_lse, o,
 // lse, stream) -> o or (o, lse); scale and max_len None: D^-0.5 and the table's width
 PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -281,11 +331,7 @@ PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                                 sp, stream);
           }));
     if (!return_lse) return THPVariable_Wrap(o);
-    PyObject *out = PyTuple_New(2);
-    if (!out) throw Raised{};
-    PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(o));
-    PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(lse));
-    return out;
+    return pair(o, lse);
   });
 }
 
@@ -298,6 +344,7 @@ PyObject *set_status_check(PyObject *, PyObject *f) {
 PyMethodDef methods[] = {
     {"add_rmsnorm", (PyCFunction)(void (*)())add_rmsnorm, METH_FASTCALL, nullptr},
     {"rope_append", (PyCFunction)(void (*)())rope_append, METH_FASTCALL, nullptr},
+    {"norm_rope_append", (PyCFunction)(void (*)())norm_rope_append, METH_FASTCALL, nullptr},
     {"paged_decode", (PyCFunction)(void (*)())paged_decode, METH_FASTCALL, nullptr},
     {"set_status_check", set_status_check, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
