@@ -519,6 +519,68 @@ fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache
                                        hipStream_t stream);
 
 /*
+ * Attention of whole prompts over their own keys, packed one behind the other.
+ *
+ *   q [T,Hq,D], k, v [T,Hkv,D] bf16  by strides in values (token, head; a head's D
+ *                                    values lie together): views of a QKV projection
+ *                                    will do.  Strides are multiples of 8, 0 .. 2^36;
+ *                                    Hq a multiple of Hkv: query head n reads key
+ *                                    head n / (Hq / Hkv)
+ *   starts [B+1] int32               prompt b is rows starts[b] .. starts[b+1] - 1:
+ *                                    nondecreasing, 0 .. T (others are clamped: such
+ *                                    prompts' rows are unspecified); 4-byte aligned
+ *   scale, softcap, window           score = scale (q . k); with softcap > 0,
+ *                                    softcap tanh(score / softcap); |scale| <= 2^100, 0 <=
+ *                                    softcap < inf, window >= 0
+ *   causal                           not 0: token i sees tokens 0 .. i of its prompt, with
+ *                                    window > 0 the last `window` of them; 0: all
+ *                                    tokens of its prompt (window must be 0)
+ *   o [T,Hq,D] bf16                  sum_t softmax(score)_t v_t
+ *   lse [T,Hq] fp32 or NULL          log sum_t exp(score_t), natural logarithm;
+ *                                    4-byte aligned
+ * Rows of o and lse outside every prompt are left as they were.  A row whose scores are all
+ * -inf gives o = 0 and lse = -inf; keys and values that a row does not see do not
+ * reach it, whatever they hold.  Scores, softmax sums and o are held in fp32; the
+ * softmax weights enter the product with v as one bf16 each, relative to a reference
+ * that is up to 2^8 below the row's largest.  Sums are divided at the end, and may pass
+ * fp32's range where the largest |v| times the tokens that count reaches 2^120.
+ * Few rows over many keys are divided over the keys, with fp32 partials in
+ * library scratch memory that a second kernel joins in a fixed order: results are
+ * deterministic, but a row's rounding depends on the sizes of the call.
+ *   1 <= Hq, Hkv <= 1024; D is 64, 128 or 256; 0 <= T <= 2^24; T Hq D <= 2^36; B <= 65535.
+ */
+fp8l_status prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *starts, int64_t B,
+                             int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t q_token, int64_t q_head,
+                             int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, float scale,
+                             float softcap, int64_t window, int causal, uint16_t *o, float *lse, hipStream_t stream);
+
+/*
+ * Attention of the last tokens of each of B sequences over the paged cache that holds
+ * them: a chunk of a prompt, the tokens of a draft, or one new token, in any mixture.
+ *
+ *   q [T,Hq,D] bf16                  rows starts[b] .. starts[b+1] - 1 are the last tokens of
+ *                                    sequence b, in order; starts as in prompt_attention
+ *   block_table, seq_lens, max_len   as in paged_decode_attention (seq_lens counts the
+ *                                    tokens of this call)
+ * Token i of the n of sequence b is at place seq_lens[b] - n + i and sees the cache's
+ * tokens up to its own (with window > 0 the last `window` of them).  A place below 0 (more
+ * tokens than seq_lens[b]) sees nothing: o = 0 and lse = -inf.  Cache lines that no
+ * token of the call sees may hold anything.  Everything else is as in
+ * prompt_attention, page numbers as in paged_decode_attention.
+ */
+fp8l_status paged_chunk_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                                  const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,
+                                  int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t pages,
+                                  int64_t page_size, int64_t max_pages, int64_t max_len, float scale, float softcap,
+                                  int64_t window, uint16_t *o, float *lse, hipStream_t stream);
+fp8l_status paged_chunk_attention_fp8(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                                      const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                      const int32_t *seq_lens, const int32_t *starts, int64_t B, int64_t T, int64_t Hq,
+                                      int64_t Hkv, int64_t D, int64_t pages, int64_t page_size, int64_t max_pages,
+                                      int64_t max_len, float scale, float softcap, int64_t window, uint16_t *o,
+                                      float *lse, hipStream_t stream);
+
+/*
  * Frees the scratch memory the library keeps for calls made under stream
  * capture (on every device).  Call it only once no graph and no executable
  * graph that captured a library call exists, and no capture is in progress;

@@ -39,6 +39,7 @@ EXPORTS = ("fp8_quant_act", "fp8_quant_weight_block", "prune24_compress", "fp8_b
            "fp8_quant_act_tensor", "fp8_quant_act_static", "fp8_quant_weight_tensor", "prune24_compress_tensor",
            "fp8_block_gemm_noalloc", "fp8_add_rmsnorm", "fp8_add_rmsnorm_ue8m0", "kv_rope_append",
            "kv_rope_append_fp8", "kv_norm_rope_append", "kv_norm_rope_append_fp8", "paged_decode_attention", "paged_decode_attention_fp8",
+           "prompt_attention", "paged_chunk_attention", "paged_chunk_attention_fp8",
            "fp8lin_release_graph_scratch", "fp8lin_status_str")
 MAX_LINEAR_M = 64  # the fused-quantization calls take decode-sized batches
 
@@ -97,6 +98,9 @@ def load_library():
             "kv_norm_rope_append_fp8": [P, P, P, F, P, P, P, I, I, I, I, I, B, I, I, I, P, P, P, P, P, P, P],
             "paged_decode_attention": [P, P, P, P, P, I, I, I, I, I, I, I, I, F, F, I, P, P, P],
             "paged_decode_attention_fp8": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, F, I, P, P, P],
+            "prompt_attention": [P, P, P, P, *[I] * 11, F, F, I, B, P, P, P],
+            "paged_chunk_attention": [P, P, P, P, P, P, *[I] * 9, F, F, I, P, P, P],
+            "paged_chunk_attention_fp8": [P, P, P, P, P, P, P, P, *[I] * 9, F, F, I, P, P, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -503,3 +507,31 @@ def paged_decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     """paged_decode_attention over an e4m3 cache: codes [pages,Hkv,page,D] and fp32 scales [pages,Hkv,page]."""
     return _marshal_module().paged_decode(True, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
                                           softcap, window, max_len, return_lse, o, lse, _stream_of(q))
+
+
+def prompt_attention(q, k, v, starts, scale=None, softcap: float = 0.0, window: int = 0, causal: bool = True,
+                     return_lse: bool = False, o=None, lse=None):
+    """Attention of packed prompts over their own keys: q [T,Hq,D], k and v [T,Hkv,D] bf16 (strided views will do, the
+    values of a head together), prompt b in rows starts[b] .. starts[b+1]-1 (int32 [B+1]).  scale: D^-0.5 by default;
+    softcap > 0 caps the scores; causal: a token sees its prompt up to itself, with window > 0 the last `window` tokens of
+    that, otherwise all of its prompt.  Rows outside every prompt are left as they were.  Returns o [T,Hq,D] bf16, or
+    (o, lse [T,Hq] fp32)."""
+    return _marshal_module().prompt(q, k, v, starts, scale, softcap, window, causal, return_lse, o, lse, _stream_of(q))
+
+
+def paged_chunk_attention(q, k_cache, v_cache, block_table, seq_lens, starts, scale=None, softcap: float = 0.0,
+                          window: int = 0, max_len=None, return_lse: bool = False, o=None, lse=None):
+    """Attention of the last tokens of each sequence over the paged cache that holds them: rows starts[b] ..
+    starts[b+1]-1 (int32 [B+1]) of q [T,Hq,D] bf16 are the last of the seq_lens[b] tokens of sequence b; each sees the
+    cache up to itself.  Other arguments as in paged_decode_attention; rows of o and lse outside every sequence are left
+    as they were.  Returns o [T,Hq,D] bf16, or (o, lse [T,Hq] fp32)."""
+    return _marshal_module().paged_chunk(False, q, k_cache, v_cache, None, None, block_table, seq_lens, starts, scale,
+                                         softcap, window, max_len, return_lse, o, lse, _stream_of(q))
+
+
+def paged_chunk_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, starts, scale=None,
+                              softcap: float = 0.0, window: int = 0, max_len=None, return_lse: bool = False, o=None,
+                              lse=None):
+    """paged_chunk_attention over an e4m3 cache: codes [pages,Hkv,page,D] and fp32 scales [pages,Hkv,page]."""
+    return _marshal_module().paged_chunk(True, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, starts,
+                                         scale, softcap, window, max_len, return_lse, o, lse, _stream_of(q))

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libfp8lin.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "quant.hip", "prune24.hip", "gemm_dense.hip", "gemm_sparse.hip", "workspace.hip",
-           "fixed_scratch.hip", "api_layer.hip", "norm.hip", "kv_append.hip", "paged_decode.hip"]
+           "fixed_scratch.hip", "api_layer.hip", "norm.hip", "kv_append.hip", "paged_decode.hip",
+           "prompt_attention.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -129,6 +129,75 @@ fp8l_status decode(const DecodeArgs &in, int64_t B, int64_t Hq, int64_t Hkv, int
   return finished(e, sc);
 }
 
+constexpr int64_t kMaxStride = int64_t(1) << 36;
+constexpr float kMaxScale = 0x1p100f;
+
+bool bad_scores(float scale, float softcap, int64_t window) {
+  return !(std::fabs(scale) <= kMaxScale) || !(softcap >= 0.0f) || std::isinf(softcap) || window < 0;
+}
+
+bool bad_stride(int64_t s) { return s < 0 || s > kMaxStride || s % 8 != 0; }
+
+// The attention of several tokens: the arguments that both calls have, already checked.
+fp8l_status prompt(PromptArgs a, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                   hipStream_t stream) {
+  if (fp8l_status st = check_device()) return st;
+  a.B = (int)B;
+  a.T = (int)T;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.D = (int)D;
+  a.window = (int)(window < kMaxTokens ? window : kMaxTokens);
+  // a smaller cap has no reciprocal, and leaves scores that no exponential tells from 0 either
+  if (a.softcap > 0.0f && a.softcap < 1e-30f) a.softcap = 1e-30f;
+  CallScratch sc;
+  if (hipError_t e = sc.acquire(prompt_partial_bytes(a, device_cu_count()), 0, stream)) return launched(e);
+  const hipError_t e = launch_prompt_attention(a, sc.partials(), stream);
+  return finished(e, sc);
+}
+
+bool bad_tokens(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
+  return Hq % Hkv != 0 || B < 0 || B > kMaxBatch || T < 0 || T > kMaxDim || T * Hq * D > kMaxElems;
+}
+
+fp8l_status chunk(PromptArgs a, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t pages,
+                  int64_t page_size, int64_t max_pages, int64_t max_len, int64_t window, bool fp8,
+                  hipStream_t stream) {
+  if (bad_cache(Hq, Hkv, D, pages, page_size) || bad_tokens(B, T, Hq, Hkv, D) || max_pages <= 0 ||
+      max_pages > kMaxTokens || max_pages * page_size > kMaxTokens || max_len < 0 || max_len > max_pages * page_size ||
+      bad_scores(a.scale, a.softcap, window))
+    return FP8L_ERR_SHAPE;
+  if (B == 0 || T == 0) return FP8L_OK;
+  if (!a.q || !a.k || !a.v || !a.block_table || !a.seq_lens || !a.starts || !a.o ||
+      (fp8 && (!a.k_scale || !a.v_scale)))
+    return FP8L_ERR_NULL;
+  const void *ptrs[] = {a.q, a.k, a.v, a.k_scale, a.v_scale, a.o};
+  for (const void *p : ptrs)
+    if (!aligned16(p)) return FP8L_ERR_ALIGN;
+  if (((uintptr_t)a.block_table & 3u) || ((uintptr_t)a.seq_lens & 3u) || ((uintptr_t)a.starts & 3u) ||
+      ((uintptr_t)a.lse & 3u))
+    return FP8L_ERR_ALIGN;
+  const int64_t lines = pages * page_size * Hkv, cache_bytes = lines * D * (fp8 ? 1 : 2);
+  const Range ins[] = {{a.q, T * Hq * D * 2},
+                       {a.k, cache_bytes},
+                       {a.v, cache_bytes},
+                       {a.k_scale, fp8 ? lines * 4 : 0},
+                       {a.v_scale, fp8 ? lines * 4 : 0},
+                       {a.block_table, B * max_pages * 4},
+                       {a.seq_lens, B * 4},
+                       {a.starts, (B + 1) * 4}};
+  const Range outs[] = {{a.o, T * Hq * D * 2}, {a.lse, a.lse ? T * Hq * 4 : 0}};
+  if (any_alias(outs, 2, ins, 8)) return FP8L_ERR_ALIAS;
+  a.q_token = Hq * D;
+  a.q_head = D;
+  a.pages = (int)pages;
+  a.page_size = (int)page_size;
+  a.max_pages = (int)max_pages;
+  a.max_len = (int)max_len;
+  a.causal = true;
+  return prompt(a, B, T, Hq, Hkv, D, window, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -260,6 +329,86 @@ fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache
   a.o = o;
   a.lse = lse;
   return decode(a, B, Hq, Hkv, D, pages, page_size, max_pages, max_len, window, true, stream);
+}
+
+fp8l_status prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *starts, int64_t B,
+                             int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t q_token, int64_t q_head,
+                             int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, float scale,
+                             float softcap, int64_t window, int causal, uint16_t *o, float *lse, hipStream_t stream) {
+  if (bad_cache(Hq, Hkv, D, 1, 16) || bad_tokens(B, T, Hq, Hkv, D) || bad_scores(scale, softcap, window) ||
+      (window > 0 && !causal) || bad_stride(q_token) || bad_stride(q_head) || bad_stride(k_token) ||
+      bad_stride(k_head) || bad_stride(v_token) || bad_stride(v_head))
+    return FP8L_ERR_SHAPE;
+  if (B == 0 || T == 0) return FP8L_OK;
+  if (!q || !k || !v || !starts || !o) return FP8L_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || ((uintptr_t)starts & 3u) ||
+      ((uintptr_t)lse & 3u))
+    return FP8L_ERR_ALIGN;
+  const Range ins[] = {{q, ((T - 1) * q_token + (Hq - 1) * q_head + D) * 2},
+                       {k, ((T - 1) * k_token + (Hkv - 1) * k_head + D) * 2},
+                       {v, ((T - 1) * v_token + (Hkv - 1) * v_head + D) * 2},
+                       {starts, (B + 1) * 4}};
+  const Range outs[] = {{o, T * Hq * D * 2}, {lse, lse ? T * Hq * 4 : 0}};
+  if (any_alias(outs, 2, ins, 4)) return FP8L_ERR_ALIAS;
+  PromptArgs a{};
+  a.q = q;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.k = k;
+  a.v = v;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.starts = starts;
+  a.max_len = (int)T;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.causal = causal != 0;
+  a.o = o;
+  a.lse = lse;
+  return prompt(a, B, T, Hq, Hkv, D, window, stream);
+}
+
+fp8l_status paged_chunk_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                                  const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,
+                                  int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t pages,
+                                  int64_t page_size, int64_t max_pages, int64_t max_len, float scale, float softcap,
+                                  int64_t window, uint16_t *o, float *lse, hipStream_t stream) {
+  PromptArgs a{};
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.starts = starts;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.o = o;
+  a.lse = lse;
+  return chunk(a, B, T, Hq, Hkv, D, pages, page_size, max_pages, max_len, window, false, stream);
+}
+
+fp8l_status paged_chunk_attention_fp8(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                                      const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                      const int32_t *seq_lens, const int32_t *starts, int64_t B, int64_t T, int64_t Hq,
+                                      int64_t Hkv, int64_t D, int64_t pages, int64_t page_size, int64_t max_pages,
+                                      int64_t max_len, float scale, float softcap, int64_t window, uint16_t *o,
+                                      float *lse, hipStream_t stream) {
+  PromptArgs a{};
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.starts = starts;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.o = o;
+  a.lse = lse;
+  return chunk(a, B, T, Hq, Hkv, D, pages, page_size, max_pages, max_len, window, true, stream);
 }
 
 }  // extern "C"

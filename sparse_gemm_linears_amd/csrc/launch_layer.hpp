@@ -57,4 +57,27 @@ hipError_t launch_paged_decode(const DecodeArgs &a, float *part, hipStream_t str
 // (0 where one workgroup covers a whole sequence).
 size_t paged_decode_partial_bytes(const DecodeArgs &a, int cus);
 
+// Attention of several tokens of each sequence: over their own keys (k and v given by
+// strides), or over a paged cache (block_table given).
+struct PromptArgs {
+  const uint16_t *q;
+  int64_t q_token, q_head;  // strides in values
+  const void *k, *v;        // bf16, or e4m3 codes of a cache when the scales are given
+  int64_t k_token, k_head, v_token, v_head;  // strides in values; not used for a cache
+  const float *k_scale, *v_scale;
+  const int32_t *starts;  // rows of sequence b: starts[b] .. starts[b + 1] - 1
+  const int32_t *block_table, *seq_lens;  // both NULL without a cache
+  int B, T, Hq, Hkv, D;
+  int pages, page_size, max_pages;
+  int max_len;           // most keys of a sequence
+  float scale, softcap;  // softcap 0: none
+  int window;            // 0: none
+  bool causal;
+  uint16_t *o;
+  float *lse;  // may be NULL
+};
+hipError_t launch_prompt_attention(const PromptArgs &a, float *part, hipStream_t stream);
+// Bytes of fp32 partials that call needs on a device with `cus` compute units.
+size_t prompt_partial_bytes(const PromptArgs &a, int cus);
+
 }  // namespace fp8lin

@@ -58,6 +58,28 @@ const Tensor &want(PyObject *o, const char *name, at::ScalarType type, Sizes siz
   return t;
 }
 
+// A bf16 tensor [tokens, heads, D] on the current device whose heads lie together, with
+// any other strides; those of a dimension of one are not used.
+const Tensor &want_heads(PyObject *o, const char *name, int64_t &token, int64_t &head) {
+  if (!THPVariable_Check(o)) raise(PyExc_TypeError, std::string(name) + ": expected a torch.Tensor");
+  const Tensor &t = THPVariable_Unpack(o);
+  if (t.scalar_type() != at::kBFloat16)
+    raise(PyExc_TypeError, std::string(name) + ": expected dtype BFloat16, got " + c10::toString(t.scalar_type()));
+  if (!t.is_cuda()) raise(PyExc_ValueError, std::string(name) + ": expected a device tensor");
+  if (t.dim() != 3)
+    raise(PyExc_ValueError, std::string(name) + ": expected 3 dimensions, got " + text_of(t.sizes()));
+  int current = -1;
+  if (hipGetDevice(&current) != hipSuccess || t.get_device() != current)
+    raise(PyExc_ValueError, std::string(name) + ": expected a tensor on the current device");
+  if (t.size(2) > 1 && t.stride(2) != 1)
+    raise(PyExc_ValueError, std::string(name) + ": expected the values of a head to lie together");
+  token = t.size(0) > 1 ? t.stride(0) : 0;
+  head = t.size(1) > 1 ? t.stride(1) : 0;
+  if (token % 8 || head % 8)
+    raise(PyExc_ValueError, std::string(name) + ": expected strides of whole 16 bytes, got " + text_of(t.strides()));
+  return t;
+}
+
 // want() for a tensor of `dims` dimensions.
 const Tensor &want_dims(PyObject *o, const char *name, at::ScalarType type, int64_t dims,
                         at::ScalarType bytes = at::ScalarType::Undefined) {
@@ -335,6 +357,88 @@ PyObject *paged_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// starts [B + 1] of B sequences.
+const Tensor &want_starts(PyObject *o, int64_t *B) {
+  const Tensor &t = want_dims(o, "starts", at::kInt, 1);
+  if (t.size(0) < 1) raise(PyExc_ValueError, "starts: expected one number more than there are sequences");
+  *B = t.size(0) - 1;
+  return t;
+}
+
+// (q, k, v, starts, scale, softcap, window, causal, return_lse, o, lse, stream) -> o or (o, lse); scale None: D^-0.5
+PyObject *prompt(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject * {
+    int64_t qt, qh, kt, kh, vt, vh, B;
+    const Tensor &q = want_heads(a[0], "q", qt, qh), &k = want_heads(a[1], "k", kt, kh),
+                 &v = want_heads(a[2], "v", vt, vh);
+    const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = k.size(1);
+    if (k.size(0) != T || k.size(2) != D)
+      raise(PyExc_ValueError, "k: expected heads of the tokens of q, got " + text_of(k.sizes()));
+    if (v.sizes() != k.sizes()) raise(PyExc_ValueError, "v: expected the sizes of k, got " + text_of(v.sizes()));
+    const Tensor &starts = want_starts(a[3], &B);
+    const float scale = given(a[4]) ? (float)real(a[4]) : (float)(1.0 / std::sqrt((double)D));
+    const float softcap = (float)real(a[5]);
+    const int64_t window = whole(a[6]);
+    const int causal = truth(a[7]);
+    const bool return_lse = truth(a[8]);
+    const Tensor o = output(a[9], "o", at::kBFloat16, {T, Hq, D}, q);
+    Tensor lse;
+    if (return_lse || given(a[10])) lse = output(a[10], "lse", at::kFloat, {T, Hq}, q);
+    hipStream_t stream = stream_of(a[11]);
+    const auto *qp = data<uint16_t>(q), *kp = data<uint16_t>(k), *vp = data<uint16_t>(v);
+    const auto *sp = data<int32_t>(starts);
+    auto *op = data<uint16_t>(o);
+    auto *lp = data<float>(lse);
+    check("prompt_attention", unlocked([&] {
+            return prompt_attention(qp, kp, vp, sp, B, T, Hq, Hkv, D, qt, qh, kt, kh, vt, vh, scale, softcap, window,
+                                    causal, op, lp, stream);
+          }));
+    if (!return_lse) return THPVariable_Wrap(o);
+    return pair(o, lse);
+  });
+}
+
+// (fp8, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, starts, scale, softcap, window, max_len,
+// return_lse, o, lse, stream) -> o or (o, lse); scale and max_len None: D^-0.5 and the table's width
+PyObject *paged_chunk(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject * {
+    const bool fp8 = truth(a[0]), return_lse = truth(a[13]);
+    const Cache c = want_cache(a + 2, fp8);
+    const Tensor &q = want_dims(a[1], "q", at::kBFloat16, 3);
+    const int64_t T = q.size(0), Hq = q.size(1);
+    if (q.size(2) != c.dim)
+      raise(PyExc_ValueError, "q: expected heads of " + std::to_string(c.dim) + ", got " + text_of(q.sizes()));
+    int64_t B;
+    const Tensor &starts = want_starts(a[8], &B);
+    const Tensor &table = want_dims(a[6], "block_table", at::kInt, 2);
+    if (table.size(0) != B)
+      raise(PyExc_ValueError, "block_table: expected " + std::to_string(B) + " rows, got " + text_of(table.sizes()));
+    const Tensor &lens = want(a[7], "seq_lens", at::kInt, {B});
+    const int64_t max_pages = table.size(1);
+    const float scale = given(a[9]) ? (float)real(a[9]) : (float)(1.0 / std::sqrt((double)c.dim));
+    const float softcap = (float)real(a[10]);
+    const int64_t window = whole(a[11]), max_len = given(a[12]) ? whole(a[12]) : max_pages * c.page;
+    const Tensor o = output(a[14], "o", at::kBFloat16, {T, Hq, c.dim}, q);
+    Tensor lse;
+    if (return_lse || given(a[15])) lse = output(a[15], "lse", at::kFloat, {T, Hq}, q);
+    hipStream_t stream = stream_of(a[16]);
+    const auto *qp = data<uint16_t>(q);
+    const auto *tp = data<int32_t>(table), *np = data<int32_t>(lens), *sp = data<int32_t>(starts);
+    auto *op = data<uint16_t>(o);
+    auto *lp = data<float>(lse);
+    check(fp8 ? "paged_chunk_attention_fp8" : "paged_chunk_attention", unlocked([&] {
+            return fp8 ? paged_chunk_attention_fp8(qp, data<uint8_t>(c.k), data<uint8_t>(c.v), data<float>(c.ks),
+                                                   data<float>(c.vs), tp, np, sp, B, T, Hq, c.heads, c.dim, c.pages,
+                                                   c.page, max_pages, max_len, scale, softcap, window, op, lp, stream)
+                       : paged_chunk_attention(qp, data<uint16_t>(c.k), data<uint16_t>(c.v), tp, np, sp, B, T, Hq,
+                                               c.heads, c.dim, c.pages, c.page, max_pages, max_len, scale, softcap,
+                                               window, op, lp, stream);
+          }));
+    if (!return_lse) return THPVariable_Wrap(o);
+    return pair(o, lse);
+  });
+}
+
 PyObject *set_status_check(PyObject *, PyObject *f) {
   Py_INCREF(f);
   Py_XSETREF(g_status_check, f);
@@ -346,6 +450,8 @@ PyMethodDef methods[] = {
     {"rope_append", (PyCFunction)(void (*)())rope_append, METH_FASTCALL, nullptr},
     {"norm_rope_append", (PyCFunction)(void (*)())norm_rope_append, METH_FASTCALL, nullptr},
     {"paged_decode", (PyCFunction)(void (*)())paged_decode, METH_FASTCALL, nullptr},
+    {"prompt", (PyCFunction)(void (*)())prompt, METH_FASTCALL, nullptr},
+    {"paged_chunk", (PyCFunction)(void (*)())paged_chunk, METH_FASTCALL, nullptr},
     {"set_status_check", set_status_check, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,0 +1,580 @@
+// Attention of several tokens of each sequence: of packed prompts over their own keys, or
+// of the last tokens of each sequence over a paged key-value cache.
+//
+// For query head n of a token at place p of its sequence, over the keys t that it sees
+// (t <= p where causal, the last `window` of them, or all): score_t = scale q.k_t, capped as
+// c tanh(score / c) when a cap is given, o = sum_t softmax(score)_t v_t and
+// lse = log sum_t exp(score_t), in one pass with a running maximum and sum.
+//
+// Bound: the matrix rate for long chunks (4 D flops for each query head and key against
+// 4 D bytes for each key head and key of a whole block of rows), the cache's bytes for
+// chunks of a few tokens.  The query heads of a key head share its keys: a row is a token
+// and one of these heads (row = token * group + head), so that a block of rows reads each
+// key once for all of them and a short chunk still fills a wave's rows.
+//
+// A wave holds 32 rows, a workgroup of 1 to 4 waves 32 to 128; tiles of 64 keys (32 for
+// D = 256) go through LDS, copied past the registers while the tile before is used, two
+// buffers each.  Layouts (v_mfma_f32_32x32x16_bf16: lane l, n = l % 32, h = l / 32):
+//   scores   A = K: row n is key n, B = Q: column n is a row; lane half h holds values
+//            16 s + 8 h .. + 7 of step s;
+//   weights  the scores come out with column n = row and register i = key
+//            8 (i / 4) + 4 h + i % 4: a row's maximum and sum stay in two lanes, and registers
+//            8 s .. 8 s + 7 are the B operand of the second product's step s if its 16
+//            keys are counted in that order;
+//   values   A = V transposed, read from LDS by ds_read_b64_tr_b16 (16 lanes take 4 keys
+//            of 16 values; lane i gets value i of the four).
+// The weights enter the second product as one bf16 each (2^-9 relative, as much as the
+// output's own rounding when one key counts, and less the more there are); sums of
+// weights are of the fp32 values.
+//
+// LDS rows are whole lines of a head; 16-byte chunks of a row are permuted by key_swizzle
+// and value_swizzle so that 16 rows of one column of K, and 8 rows of four columns
+// of V, lie in different banks.
+#include <cmath>
+#include <type_traits>
+
+#include "device_common.hpp"
+#include "gemm_common.hpp"
+#include "launch.hpp"
+#include "launch_layer.hpp"
+#include "prompt_plan.hpp"
+
+namespace fp8lin {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+__device__ __forceinline__ v8bf as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(v8bf, (v4u{a, b, c, d}));
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int from_lane(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
+  return (int64_t)(uint32_t)from_lane((int)x, lane) | (int64_t)from_lane((int)(x >> 32), lane) << 32;
+}
+
+#define FP8LIN_INLINE __attribute__((always_inline))
+
+enum class Source { kRows, kCache, kCodes };  // strided bf16 rows, a bf16 cache, an e4m3 cache
+
+// Position of 16-byte chunk c of row r in an LDS row of D values.
+template <int D>
+__device__ __forceinline__ int key_swizzle(int r, int c) {
+  return c ^ (D == 64 ? (r >> 1) & 7 : r & 15);
+}
+template <int D>
+__device__ __forceinline__ int value_swizzle(int r, int c) {
+  return c ^ (D == 64 ? (r >> 1 & 1) << 2 : (r & 3) << 2);
+}
+
+// A block of rows: rows row0 .. row0 + block rows - 1 of the `rows` of sequence b, whose
+// first token is `start`; tokens first .. last of it.
+struct Block {
+  int b, start, tokens, row0, rows;
+  int begin, end;  // keys that some row of the block sees (begin rounded down to 16)
+  int lowest;      // the first of them
+  int place0;      // place of the sequence's first token among the keys
+  int tiles;
+};
+
+__device__ __forceinline__ int start_of(const PromptArgs &a, int b) { return min(max(a.starts[b], 0), a.T); }
+
+// Finds block `number` of the batch; false if the number is not used.
+__device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, int block_rows, int tile_keys,
+                                           Block &k) {
+  const int lane = threadIdx.x & 63, group = a.Hq / a.Hkv;
+  // the last sequence whose numbers start at `number` or before, 64 candidates at a time
+  int low = 0, high = a.B;
+  while (high - low > 1 || low == 0) {
+    const int step = (high - low + 63) / 64, b = low + lane * step;
+    const bool before = b < high && first_block(start_of(a, min(b, a.B - 1)), b, group, block_rows) <= number;
+    const int count = __popcll(__ballot(before));
+    if (count == 0) return false;
+    low += (count - 1) * step;
+    high = min(high, low + step);
+    if (step == 1) break;
+  }
+  k.b = uniform(low);
+  k.start = uniform(start_of(a, k.b));
+  k.tokens = uniform(start_of(a, k.b + 1)) - k.start;
+  const int64_t row0 = (number - first_block(k.start, k.b, group, block_rows)) * block_rows;
+  if (k.tokens <= 0 || row0 < 0 || row0 >= (int64_t)k.tokens * group) return false;
+  k.row0 = (int)row0;
+  k.rows = k.tokens * group;
+  const int first = k.row0 / group, last = min(k.row0 + block_rows, k.rows) - 1;
+  const int keys = a.block_table ? uniform(min(max(a.seq_lens[k.b], 0), a.max_len)) : k.tokens;
+  k.place0 = keys - k.tokens;
+  k.end = a.causal ? max(0, k.place0 + last / group + 1) : keys;
+  k.lowest = a.window > 0 ? max(0, k.place0 + first - a.window + 1) : 0;
+  k.begin = k.lowest & ~15;
+  k.tiles = (max(0, k.end - k.begin) + tile_keys - 1) / tile_keys;
+  return true;
+}
+
+// c tanh(x / c) of each value.  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that would
+// lose a small score's low bits, its power series (2^-26 of it is left out).
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], float cap) {
+  const float rate = 1.f / cap;
+  float most = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; j++) most = fmaxf(most, fabsf(x[j] * rate));
+  const bool large = __any(!(most < 0.25f));
+#pragma unroll
+  for (int j = 0; j < N; j++) {
+    const float z = x[j] * rate, u = z * z;
+    float t = __builtin_fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+    t = __builtin_fmaf(u, t, 2.f / 15.f);
+    t = __builtin_fmaf(u, t, -1.f / 3.f);
+    float y = cap * __builtin_fmaf(z * u, t, z);
+    if (large) {
+      const float m = fabsf(z), e = __builtin_amdgcn_exp2f(2.f * kLog2e * m);
+      if (!(m < 0.25f)) y = cap * copysignf(1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e), z);
+    }
+    x[j] = y;
+  }
+}
+
+template <int D, Source SRC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, PromptPlan plan, float *part) {
+  constexpr bool kPaged = SRC != Source::kRows, kFp8 = SRC == Source::kCodes;
+  constexpr int KT = prompt_tile_keys(D), S = KT / 32, kRow = 2 * D;  // bytes of an LDS row
+  constexpr int kBlockRows = WAVES * kWaveRows, kChunks = D / 8;
+  __shared__ __align__(1024) uint8_t lds_k0[KT * kRow], lds_k1[KT * kRow], lds_v0[KT * kRow], lds_v1[KT * kRow];
+  __shared__ __align__(16) float lds_s0[kFp8 ? 2 * KT : 1], lds_s1[kFp8 ? 2 * KT : 1];
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), n = lane & 31, h = lane >> 5;
+  const int group = a.Hq / a.Hkv;
+  const uint32_t self = (uint32_t)plan.first + blockIdx.x, rest = self / (uint32_t)a.Hkv;
+  const int kvh = (int)(self - rest * (uint32_t)a.Hkv);
+  const int split = (int)(rest % (uint32_t)plan.splits);
+  const int64_t number = plan.blocks - 1 - (int)(rest / (uint32_t)plan.splits);  // a sequence's longest rows first
+  Block blk;
+  if (!find_block(a, number, kBlockRows, KT, blk)) return;
+  const int tile0 = split * plan.per, tile_end = min(blk.tiles, tile0 + plan.per);
+  if (split > 0 && tile0 >= blk.tiles) return;
+
+  // the wave's rows; rows past the last one repeat it and are not stored
+  const int wave_row = blk.row0 + wave * kWaveRows;
+  const bool working = wave_row < blk.rows;
+  const int row = min(wave_row + n, blk.rows - 1), token = row / group, head = kvh * group + row % group;
+  auto low_of = [&](int place) { return a.window > 0 ? place - a.window + 1 : 0; };
+  const int place = blk.place0 + token;
+  const int seen_end = a.causal ? place + 1 : blk.end, seen_low = low_of(place);
+  // of the wave's first and last row
+  const int first_place = blk.place0 + min(wave_row, blk.rows - 1) / group;
+  const int last_place = blk.place0 + (min(wave_row + kWaveRows, blk.rows) - 1) / group;
+  const int all_end = a.causal ? first_place + 1 : blk.end;                    // keys before it are seen by all rows
+  const int all_low = low_of(last_place);
+  const int any_end = a.causal ? last_place + 1 : blk.end, any_low = low_of(first_place);
+
+  v8bf qf[D / 16];
+  {
+    const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)head * a.q_head + 8 * h;
+    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;  // the weights' exponents grow with the scores
+#pragma unroll
+    for (int s = 0; s < D / 16; s++) {
+      const uint4 raw = *reinterpret_cast<const uint4 *>(src + 16 * s);
+      qf[s] = as_bf16x8(raw.x ^ sign, raw.y ^ sign, raw.z ^ sign, raw.w ^ sign);
+    }
+  }
+  v16f o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; i++)
+#pragma unroll
+    for (int j = 0; j < 16; j++) o[i][j] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float scale = fabsf(a.scale);
+
+  // Copies.  A wave's copy of 64 x 16 bytes covers a few rows, all in one run of 16 keys (which
+  // lies in one page).  Keys that no row sees may hold anything, so their rows repeat
+  // the nearest key that is seen.
+  int64_t found = 0;   // of a cache: lane x holds the line of run x of the next 64 runs
+  int found_from = 0;  // key of run 0
+  auto look_up = [&](int key0) FP8LIN_INLINE {
+    found_from = key0;
+    const int key = key0 + 16 * lane;
+    if (key < blk.end) {
+      const int p = (int)((uint32_t)key / (uint32_t)a.page_size);
+      const int page = min(max(a.block_table[(int64_t)blk.b * a.max_pages + p], 0), a.pages - 1);
+      found = ((int64_t)page * a.Hkv + kvh) * a.page_size + (key - p * a.page_size);
+    }
+  };
+  // line (in a cache) of the run of keys with tile row r of the tile at key0
+  auto run_line = [&](int key0, int r) { return from_lane(found, (key0 - found_from) / 16 + (r >> 4)); };
+
+  constexpr int kCopyRows = 512 / D;  // rows of a wave's copy of bf16 values
+  constexpr int kCopies = KT / kCopyRows, kCopiesPer = (kCopies + WAVES - 1) / WAVES;
+  auto copy_tile = [&](int key0, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
+    const int last = blk.end - 1 - key0, lowest = blk.lowest - key0;  // tile rows of the keys that are seen
+#pragma unroll
+    for (int i = 0; i < kCopiesPer; i++) {
+      const int r0 = (i * WAVES + wave) * kCopyRows;
+      if (kCopies % WAVES != 0 && r0 >= KT) break;
+      const int r = r0 + lane / kChunks, c = lane % kChunks;
+      const int src = max(min(r, last), lowest);
+      const int kc = key_swizzle<D>(r, c) * 8, vc = value_swizzle<D>(r, c) * 8;
+      const uint16_t *kp, *vp;
+      if constexpr (kPaged) {
+        const int64_t line = run_line(key0, min(r0, last)) * D;
+        kp = static_cast<const uint16_t *>(a.k) + line + ((src & 15) * D + kc);
+        vp = static_cast<const uint16_t *>(a.v) + line + ((src & 15) * D + vc);
+      } else {
+        const int64_t t = blk.start + key0 + src;
+        kp = static_cast<const uint16_t *>(a.k) + t * a.k_token + (int64_t)kvh * a.k_head + kc;
+        vp = static_cast<const uint16_t *>(a.v) + t * a.v_token + (int64_t)kvh * a.v_head + vc;
+      }
+      copy16_global_to_lds(kp, lk + r0 * kRow);
+      copy16_global_to_lds(vp, lv + r0 * kRow);
+    }
+  };
+  // e4m3 codes go through registers: 16 codes of a lane become 32 bytes of bf16
+  constexpr int kCodeRows = 1024 / D, kLoads = KT / kCodeRows, kLoadsPer = (kLoads + WAVES - 1) / WAVES;
+  uint4 raw_k[kFp8 ? kLoadsPer : 1], raw_v[kFp8 ? kLoadsPer : 1];
+  float raw_s[kFp8 && WAVES == 1 ? 2 : 1];
+  auto load_codes = [&](int key0) FP8LIN_INLINE {
+    const int last = blk.end - 1 - key0, lowest = blk.lowest - key0;
+#pragma unroll
+    for (int i = 0; i < kLoadsPer; i++) {
+      const int r0 = (i * WAVES + wave) * kCodeRows;
+      if (kLoads % WAVES != 0 && r0 >= KT) break;
+      const int r = r0 + lane / (D / 16), c = lane % (D / 16);
+      const int src = max(min(r, last), lowest);
+      const int64_t at = run_line(key0, min(r0, last)) * D + ((src & 15) * D + 16 * c);
+      raw_k[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.k) + at);
+      raw_v[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.v) + at);
+    }
+    // the scales: wave 0 the keys', the last wave the values'
+    if (wave == 0 || wave == WAVES - 1) {
+      const int src = max(min(lane & (KT - 1), last), lowest);
+      const int64_t at = __shfl(found, (key0 - found_from) / 16 + (src >> 4), 64) + (src & 15);
+      raw_s[0] = (wave == 0 ? a.k_scale : a.v_scale)[at];
+      if constexpr (WAVES == 1) raw_s[kFp8 ? 1 : 0] = a.v_scale[at];
+    }
+  };
+  auto store_codes = [&](uint8_t *lk, uint8_t *lv, float *ls) FP8LIN_INLINE {
+    auto put = [&](const uint4 &raw, uint8_t *row_at, int c0, int c1) FP8LIN_INLINE {
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      uint32_t b[8];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        b[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.0f, false));
+        b[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.0f, true));
+      }
+      *reinterpret_cast<uint4 *>(row_at + 16 * c0) = make_uint4(b[0], b[1], b[2], b[3]);
+      *reinterpret_cast<uint4 *>(row_at + 16 * c1) = make_uint4(b[4], b[5], b[6], b[7]);
+    };
+#pragma unroll
+    for (int i = 0; i < kLoadsPer; i++) {
+      const int r0 = (i * WAVES + wave) * kCodeRows;
+      if (kLoads % WAVES != 0 && r0 >= KT) break;
+      const int r = r0 + lane / (D / 16), c = 2 * (lane % (D / 16));
+      put(raw_k[i], lk + r * kRow, key_swizzle<D>(r, c), key_swizzle<D>(r, c + 1));
+      put(raw_v[i], lv + r * kRow, value_swizzle<D>(r, c), value_swizzle<D>(r, c + 1));
+    }
+    if (wave == 0 && lane < KT) ls[lane] = raw_s[0];
+    if (wave == WAVES - 1 && lane < KT) ls[KT + lane] = raw_s[kFp8 && WAVES == 1 ? 1 : 0];
+  };
+
+  // Reads of a tile's fragments.
+  auto key_frag = [&](const uint8_t *lk, int sub, int s) FP8LIN_INLINE {
+    const uint4 raw = *reinterpret_cast<const uint4 *>(lk + (32 * sub + n) * kRow + 16 * key_swizzle<D>(n, 2 * s + h));
+    return as_bf16x8(raw.x, raw.y, raw.z, raw.w);
+  };
+  auto value_frag = [&](uint8_t *lv, int db, int step) FP8LIN_INLINE {  // values 32 db .. + 31 of keys 16 step .. + 15
+    const int r = 4 * h + (lane & 15) / 4, c = 4 * db + 2 * (lane >> 4 & 1) + (lane & 3) / 2;
+    uint8_t *at = lv + (16 * step + r) * kRow + 16 * value_swizzle<D>(r, c) + 8 * (lane & 1);
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 8 * kRow));
+    typedef short v8s __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(v8bf, (v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}));
+  };
+
+  auto use_tile = [&](int key0, uint8_t *lk, uint8_t *lv, const float *ls) FP8LIN_INLINE {
+    v16f sc[S];
+#pragma unroll
+    for (int sub = 0; sub < S; sub++) {
+#pragma unroll
+      for (int j = 0; j < 16; j++) sc[sub][j] = 0.f;
+#pragma unroll
+      for (int s = 0; s < D / 16; s++)
+        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(lk, sub, s), qf[s], sc[sub], 0, 0, 0);
+    }
+    float x[16 * S];
+#pragma unroll
+    for (int j = 0; j < 16 * S; j++) x[j] = sc[j / 16][j % 16];
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int j = 0; j < 4 * S; j++) {
+        const float4 ks = *reinterpret_cast<const float4 *>(ls + 8 * j + 4 * h);
+        x[4 * j] *= ks.x;
+        x[4 * j + 1] *= ks.y;
+        x[4 * j + 2] *= ks.z;
+        x[4 * j + 3] *= ks.w;
+      }
+    }
+    float rate = scale * kLog2e;  // of the exponents in units of x
+    if (a.softcap > 0.f || scale == 0.f) {  // (0 times the -infinity of a hidden key would be a NaN)
+#pragma unroll
+      for (int j = 0; j < 16 * S; j++) x[j] *= scale;
+      if (a.softcap > 0.f) cap_scores(x, a.softcap);
+      rate = kLog2e;
+    }
+    const bool masked = key0 + KT > all_end || key0 < all_low;
+    const int live_end = seen_end - key0 - 4 * h, live_low = seen_low - key0 - 4 * h;
+    auto live = [&](int j) { return 8 * (j >> 2) + (j & 3) < live_end && 8 * (j >> 2) + (j & 3) >= live_low; };
+    if (masked) {
+#pragma unroll
+      for (int j = 0; j < 16 * S; j++) x[j] = live(j) ? x[j] : -INFINITY;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < 16 * S; j++) top = fmaxf(top, x[j]);
+    top *= rate;
+    // The reference of the exponents follows the maximum only when some score passes it by
+    // 2^8: weights stay below 2^8 and sums far below overflow, and most tiles need no
+    // exchange between the lane halves and no product with the factor.
+    if (__any(top > (m == -INFINITY ? -INFINITY : m + 8.f))) {
+      top = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)), m);
+      const float shrink = top == m ? 1.f : __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      l *= shrink;
+#pragma unroll
+      for (int i = 0; i < D / 32; i++) o[i] *= shrink;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < 16 * S; j++) x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], rate, -base));
+    {
+      float sum[4] = {};
+#pragma unroll
+      for (int j = 0; j < 16 * S; j++) sum[j & 3] += x[j];
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int j = 0; j < 4 * S; j++) {
+        const float4 vs = *reinterpret_cast<const float4 *>(ls + KT + 8 * j + 4 * h);
+        x[4 * j] *= vs.x;
+        x[4 * j + 1] *= vs.y;
+        x[4 * j + 2] *= vs.z;
+        x[4 * j + 3] *= vs.w;
+      }
+      if (masked) {  // a scale that is not finite belongs to no row that does not see its key
+#pragma unroll
+        for (int j = 0; j < 16 * S; j++) x[j] = live(j) ? x[j] : 0.f;
+      }
+    }
+    v8bf p[2 * S];
+#pragma unroll
+    for (int s = 0; s < 2 * S; s++)
+      p[s] = as_bf16x8(pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
+                       pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7]));
+    if (masked) {
+      // 0 times an infinity or a NaN is a NaN: a value that is not finite must not reach
+      // rows that do not see its key.
+      uint32_t odd = 0;
+      for (int i = lane; i < KT * kRow / 16; i += 64) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(lv + 16 * i);
+        odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+               ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+      }
+      if (__builtin_expect(__any((odd & 0x80008000u) != 0), 0)) {
+        // one key at a time, added where it is seen
+#pragma unroll
+        for (int s = 0; s < 2 * S; s++) {
+          for (int key = 0; key < 16; key++) {
+            const int at = 16 * s + key - 4 * h;
+            const bool seen = at < live_end && at >= live_low;
+            const uint32_t half = key & 1 ? 0xFFFF0000u : 0xFFFFu;
+            const int word = h == (key >> 2 & 1) ? (key & 3) / 2 + 2 * (key >> 3) : -1;
+            auto only = [&](const v8bf &f) FP8LIN_INLINE {
+              const v4u w = __builtin_bit_cast(v4u, f);
+              return as_bf16x8(word == 0 ? w[0] & half : 0, word == 1 ? w[1] & half : 0, word == 2 ? w[2] & half : 0,
+                               word == 3 ? w[3] & half : 0);
+            };
+            const v8bf weight = only(p[s]);
+#pragma unroll
+            for (int db = 0; db < D / 32; db++) {
+              v16f sum;
+#pragma unroll
+              for (int j = 0; j < 16; j++) sum[j] = 0.f;
+              sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(only(value_frag(lv, db, s)), weight, sum, 0, 0, 0);
+#pragma unroll
+              for (int j = 0; j < 16; j++) o[db][j] = seen ? o[db][j] + sum[j] : o[db][j];
+            }
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int db = 0; db < D / 32; db++)
+#pragma unroll
+      for (int s = 0; s < 2 * S; s++)
+        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value_frag(lv, db, s), p[s], o[db], 0, 0, 0);
+  };
+
+  auto fetch = [&](int t, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
+    const int key0 = blk.begin + t * KT;
+    if constexpr (kPaged) {
+      if (t == tile0 || key0 + KT > found_from + 1024) look_up(key0);
+    }
+    if constexpr (kFp8)
+      load_codes(key0);
+    else
+      copy_tile(key0, lk, lv);
+  };
+  auto step = [&](int t, auto stage) FP8LIN_INLINE {
+    constexpr bool kOdd = decltype(stage)::value;
+    uint8_t *lk = kOdd ? lds_k1 : lds_k0, *lv = kOdd ? lds_v1 : lds_v0;
+    float *ls = kOdd ? lds_s1 : lds_s0;
+    if constexpr (kFp8)
+      store_codes(lk, lv, ls);
+    else
+      wait_global_loads();
+    __syncthreads();
+    if (t + 1 < tile_end) fetch(t + 1, kOdd ? lds_k0 : lds_k1, kOdd ? lds_v0 : lds_v1);
+    const int key0 = blk.begin + t * KT;
+    if (working && key0 < any_end && key0 + KT > any_low) use_tile(key0, lk, lv, ls);
+  };
+  if (tile0 < tile_end) {
+    fetch(tile0, lds_k0, lds_v0);
+    for (int t = tile0; t < tile_end; t += 2) {
+      step(t, std::false_type{});
+      if (t + 1 < tile_end) step(t + 1, std::true_type{});
+    }
+  }
+
+  if (!working) return;
+  l += __shfl_xor(l, 32, 64);
+  if (wave_row + n >= blk.rows) return;
+  const int64_t out = (int64_t)(blk.start + token) * a.Hq + head;
+  if (blk.tiles <= plan.per) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t *dst = a.o + out * D + 4 * h;
+#pragma unroll
+    for (int i = 0; i < D / 8; i++) {
+      const v16f &v = o[i / 4];
+      const int j = 4 * (i % 4);
+      *reinterpret_cast<uint2 *>(dst + 8 * i) =
+          make_uint2(pack_bf16x2(v[j] * inv, v[j + 1] * inv), pack_bf16x2(v[j + 2] * inv, v[j + 3] * inv));
+    }
+    if (a.lse && h == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+  } else {
+    float *base = part + ((number * a.Hkv + kvh) * plan.splits + split) * (int64_t)prompt_part_floats(D, WAVES);
+    const int r = wave * kWaveRows + n;
+#pragma unroll
+    for (int i = 0; i < D / 8; i++) {
+      const v16f &v = o[i / 4];
+      const int j = 4 * (i % 4);
+      *reinterpret_cast<float4 *>(base + r * D + 8 * i + 4 * h) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+    if (h == 0) {
+      base[kBlockRows * D + r] = m;
+      base[kBlockRows * (D + 1) + r] = l;
+    }
+  }
+}
+
+// Joins the parts of divided blocks, in order: a wave takes a row.
+template <int D>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPlan plan, const float *part) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  const int block_rows = plan.waves * kWaveRows, group = a.Hq / a.Hkv;
+  const int64_t number = blockIdx.x / (unsigned)a.Hkv;  // few blocks are divided: one launch
+  const int kvh = (int)(blockIdx.x % (unsigned)a.Hkv);
+  Block blk;
+  if (!find_block(a, number, block_rows, prompt_tile_keys(D), blk) || blk.tiles <= plan.per) return;
+  const int parts = (blk.tiles + plan.per - 1) / plan.per;
+  const size_t floats = (size_t)block_rows * (D + 2);
+  const float *base = part + (number * a.Hkv + kvh) * plan.splits * (int64_t)floats;
+  for (int r = blockIdx.y * 4 + wave; r < min(block_rows, blk.rows - blk.row0); r += 4 * gridDim.y) {
+    float top = -INFINITY, l = 0.f, o[E] = {};
+    for (int k0 = 0; k0 < parts; k0 += 8) {  // eight parts in flight
+      float mp[8], lp[8], op[8][E];
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        const float *p = base + (size_t)min(k0 + u, parts - 1) * floats;
+        mp[u] = p[block_rows * D + r];
+        lp[u] = p[block_rows * (D + 1) + r];
+#pragma unroll
+        for (int e = 0; e < E; e++) op[u][e] = p[r * D + E * lane + e];
+      }
+      float high = top;
+#pragma unroll
+      for (int u = 0; u < 8; u++) high = fmaxf(high, mp[u]);
+      const float shrink = top == high ? 1.f : __builtin_amdgcn_exp2f(top - high);
+      top = high;
+      l *= shrink;
+#pragma unroll
+      for (int e = 0; e < E; e++) o[e] *= shrink;
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        if (k0 + u < parts) {
+          const float f = mp[u] == top ? 1.f : __builtin_amdgcn_exp2f(mp[u] - top);
+          l += lp[u] * f;
+#pragma unroll
+          for (int e = 0; e < E; e++) o[e] += op[u][e] * f;
+        }
+      }
+    }
+    const int row = blk.row0 + r;
+    const int64_t out = (int64_t)(blk.start + row / group) * a.Hq + kvh * group + row % group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; e++) a.o[out * D + E * lane + e] = (uint16_t)f32_to_bf16_rne(o[e] * inv);
+    if (a.lse && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+  }
+}
+
+template <int D, Source SRC>
+hipError_t launch(const PromptArgs &a, const PromptPlan &p, float *part, hipStream_t stream) {
+  const int64_t all = (int64_t)p.blocks * a.Hkv * p.splits;
+  PromptPlan q = p;
+  for (int64_t first = 0; first < all; first += kPromptGrid) {
+    q.first = (int)first;
+    const dim3 grid((unsigned)(all - first < kPromptGrid ? all - first : kPromptGrid)), block(64 * p.waves);
+    if (p.waves == 1)
+      hipLaunchKernelGGL((prompt_kernel<D, SRC, 1>), grid, block, 0, stream, a, q, part);
+    else if (p.waves == 2)
+      hipLaunchKernelGGL((prompt_kernel<D, SRC, 2>), grid, block, 0, stream, a, q, part);
+    else
+      hipLaunchKernelGGL((prompt_kernel<D, SRC, 4>), grid, block, 0, stream, a, q, part);
+  }
+  if (p.splits > 1) {
+    const unsigned y = (unsigned)(p.waves * kWaveRows / 16);
+    hipLaunchKernelGGL((prompt_join_kernel<D>), dim3((unsigned)p.blocks * (unsigned)a.Hkv, y), dim3(256), 0, stream, a, p,
+                       (const float *)part);
+  }
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_dim(const PromptArgs &a, const PromptPlan &p, float *part, hipStream_t stream) {
+  if (!a.block_table) return launch<D, Source::kRows>(a, p, part, stream);
+  return a.k_scale ? launch<D, Source::kCodes>(a, p, part, stream) : launch<D, Source::kCache>(a, p, part, stream);
+}
+
+}  // namespace
+
+size_t prompt_partial_bytes(const PromptArgs &a, int cus) {
+  const PromptPlan p = plan_prompt(a, cus);
+  return p.splits == 1 ? 0
+                       : (size_t)p.blocks * a.Hkv * p.splits * prompt_part_floats(a.D, p.waves) * sizeof(float);
+}
+
+hipError_t launch_prompt_attention(const PromptArgs &a, float *part, hipStream_t stream) {
+  const PromptPlan p = plan_prompt(a, device_cu_count());
+  if (a.D == 64) return launch_dim<64>(a, p, part, stream);
+  if (a.D == 128) return launch_dim<128>(a, p, part, stream);
+  return launch_dim<256>(a, p, part, stream);
+}
+
+}  // namespace fp8lin

@@ -1,0 +1,212 @@
+"""paged_chunk_attention and its e4m3 form against the 64-bit reference (tolerances in prompt_ref.py)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+from prompt_ref import Check
+from test_graph_gpu import replay_equals_eager
+from test_layer_gpu import gen, paged
+from test_prompt_gpu import starts_of
+
+pytestmark = pytest.mark.gpu
+
+
+def chunk_inputs(new, lens, Hq, Hkv, D, page, fp8, window=0, max_len=None, sharp=1.5, pages=None):
+    """Queries, a cache in which everything that no token sees is NaN, and its table; the keys and values that a
+    sequence's tokens see in 64 bits, from the first of them on."""
+    r = gen("chunk", sum(lens), sum(new), len(lens), Hq, Hkv, D, page, window)
+    # the first token of a chunk sees window - 1 keys before it
+    reach = [window + n - 1 if window and n else 0 for n in new]
+    widest = max(reach)
+    dev, table, live = paged(r, lens, Hkv, D, page, fp8, widest, pages=pages)
+    if window:  # lines of the widest reach are filled: clear what is beyond each sequence's own
+        for b, n in enumerate(lens):
+            keep = min(n, reach[b])
+            live[b] = [x[:, x.shape[1] - keep :] for x in live[b]]
+            for t in range(max(0, n - widest), n - keep):
+                for i, cleared in enumerate(dev):
+                    cleared[int(table[b, t // page]), :, t % page] = 0x7F if fp8 and i < 2 else float("nan")
+    if max_len is not None and table.shape[1] * page < max_len:  # a wider table, its entries out of range
+        more = -(-max_len // page) - table.shape[1]
+        table = torch.cat([table, torch.full((len(lens), more), -9, dtype=torch.int32, device="cuda")], 1)
+    return ref.bf16(sharp * r.standard_normal((sum(new), Hq, D))), dev, table, live
+
+
+def chunk_case(lib, new, lens, Hq, Hkv, D, page, fp8, window=0, softcap=0.0, max_len=None, scale=None, pages=None):
+    q, cache, table, live = chunk_inputs(new, lens, Hq, Hkv, D, page, fp8, window, max_len, pages=pages)
+    call = lib.paged_chunk_attention_fp8 if fp8 else lib.paged_chunk_attention
+    args = (q.cuda(), *cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), starts_of(new))
+    kw = dict(window=window, softcap=softcap, max_len=max_len, scale=scale)
+    print(f"chunk new={new[:8]} lens={lens[:8]} Hq={Hq} Hkv={Hkv} D={D} page={page} fp8={fp8} {kw}", flush=True)
+    o, lse = call(*args, **kw, return_lse=True)
+    again = call(*args, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(o, again)
+    check, at = Check(D ** -0.5 if scale is None else scale, softcap), 0
+    for b, (n, length) in enumerate(zip(new, lens)):
+        rows = slice(at, at + n)
+        k, v = live[b]
+        if n:
+            check.sequence(o[rows], lse[rows], ref.f64(q[rows]), k, v, k.shape[1] - n, window, True,
+                           f"of sequence {b}, {n} of {length}")
+        at += n
+    check.done()
+    return o, lse
+
+
+#              few over many, whole prompts, one token, none, more than there are
+NEW = [1, 3, 7, 16, 33, 64, 100, 1, 0, 5, 17, 129, 2, 4]
+LENS = [1, 3, 40, 16, 300, 65, 100, 700, 50, 0, 9, 513, 1, 1025]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(32, 8, 128, 16), (28, 4, 64, 48), (16, 1, 256, 32), (3, 3, 128, 64),
+                                           (40, 2, 128, 16), (33, 1, 64, 128), (64, 1, 128, 16), (70, 1, 256, 16),
+                                           (8, 8, 64, 16), (10, 5, 256, 1024)])
+def test_chunk_edges(gpu_lib, Hq, Hkv, D, page, fp8):
+    chunk_case(gpu_lib, NEW, LENS, Hq, Hkv, D, page, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,softcap", [(1, 0.0), (16, 0.0), (17, 30.0), (100, 0.0), (256, 5.0), (5000, 0.0),
+                                            (0, 30.0)])
+def test_chunk_window_and_cap(gpu_lib, window, softcap, fp8):
+    chunk_case(gpu_lib, NEW, LENS, 14, 2, 128, 48, fp8, window=window, softcap=softcap)
+    chunk_case(gpu_lib, [1, 20, 300], [900, 900, 900], 4, 2, 64, 16, fp8, window=window, softcap=softcap)
+    chunk_case(gpu_lib, [1, 20, 150], [700, 900, 200], 2, 1, 256, 32, fp8, window=window, softcap=softcap)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,lens,Hq,Hkv,D,page", [
+    ([7], [777], 32, 8, 128, 16), ([1], [20001], 8, 2, 128, 16), ([3, 1], [9973, 3], 8, 1, 64, 64),
+    ([4] * 4, [5000, 1, 4999, 17], 16, 16, 64, 48), ([200, 1, 2], [3000, 2500, 4000], 4, 2, 128, 64),
+    ([2], [8193], 4, 2, 256, 16), ([1], [4097], 1, 1, 128, 4096), ([512] + [1] * 9, [600] + [2000] * 9, 8, 2, 128, 32)])
+def test_chunk_long(gpu_lib, new, lens, Hq, Hkv, D, page, fp8):
+    chunk_case(gpu_lib, new, lens, Hq, Hkv, D, page, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_wider_table_and_bound(gpu_lib, fp8):
+    """A bound far above the lengths: parts of the division that have no keys."""
+    chunk_case(gpu_lib, [3, 40, 1], [30, 500, 0], 8, 2, 128, 16, fp8, max_len=60000)
+
+
+def test_one_token_is_the_decode_call(gpu_lib):
+    """One new token of each sequence: what paged_decode_attention gives, within both calls' roundings."""
+    lens = [1, 70, 300, 999]
+    q, cache, table, _ = chunk_inputs([1] * 4, lens, 8, 2, 128, 16, False)
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = gpu_lib.paged_chunk_attention(q.cuda(), *cache, table, lens_, starts_of([1] * 4), return_lse=True)
+    o2, lse2 = gpu_lib.paged_decode_attention(q.cuda(), *cache, table, lens_, return_lse=True)
+    assert ((o.float() - o2.float()).norm() / o2.float().norm()).item() < 2.0 ** -8
+    assert ((lse - lse2).abs() <= 2.0 ** -17).all()
+
+
+def test_rows_outside_every_sequence_stay(gpu_lib):
+    new, lens = [5, 0, 40], [90, 10, 64]
+    q, cache, table, _ = chunk_inputs(new, lens, 4, 2, 64, 16, True)
+    pad = torch.zeros(9, 4, 64, dtype=torch.bfloat16)
+    q = torch.cat([pad, q, pad]).cuda()
+    o = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    gpu_lib.paged_chunk_attention_fp8(q, *cache, table, lens_, starts_of(new, 9), o=o, lse=lse)
+    want = gpu_lib.paged_chunk_attention_fp8(q[9:-9], *cache, table, lens_, starts_of(new))
+    assert torch.equal(o[9:-9], want)
+    for t in (o, lse):
+        assert (t[:9] == 7).all() and (t[-9:] == 7).all() and not (t[9:-9] == 7).any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_hidden_values_of_a_cache(gpu_lib, fp8):
+    """Values and scales that are not finite reach the tokens that see them, and no token before."""
+    new, lens, at = [60], [200], 170  # a token of the chunk itself
+    q, cache, table, _ = chunk_inputs(new, lens, 4, 2, 128, 16, fp8)
+    call = gpu_lib.paged_chunk_attention_fp8 if fp8 else gpu_lib.paged_chunk_attention
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    args = (q.cuda(), *cache, table, lens_, starts_of(new))
+    want = call(*args)
+    page = int(table[0, at // 16])
+    # with an e4m3 cache: a NaN code, a NaN scale, an infinite scale
+    for bad in (["code", float("nan"), float("inf")] if fp8 else [float("nan"), float("inf"), float("-inf")]):
+        changed = cache[3 if fp8 and bad != "code" else 1]
+        kept = changed[page, :, at % 16].clone()
+        changed[page, :, at % 16] = 0x7F if bad == "code" else bad
+        o = call(*args)
+        changed[page, :, at % 16] = kept
+        before = at - (200 - 60)
+        err = (o[:before].float() - want[:before].float()).abs()
+        assert (err <= 2.0 ** -7 * want[:before].float().abs() + 2.0 ** -16).all(), bad
+        assert not torch.isfinite(o[before:]).any(), bad
+
+
+def test_bad_pages_are_clamped(gpu_lib):
+    """Page numbers out of range: such rows are unspecified, the others keep their results."""
+    new, lens = [3, 20, 4], [64, 100, 33]
+    q, cache, table, _ = chunk_inputs(new, lens, 4, 2, 64, 16, False)
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = gpu_lib.paged_chunk_attention(q.cuda(), *cache, table, lens_, starts_of(new))
+    bad = table.clone()
+    bad[1] = torch.tensor([-1, 1 << 30, -(1 << 31), (1 << 31) - 1] * 2, dtype=torch.int32, device="cuda")[: bad.shape[1]]
+    got = gpu_lib.paged_chunk_attention(q.cuda(), *cache, bad, lens_, starts_of(new))
+    assert torch.equal(got[:3], want[:3]) and torch.equal(got[23:], want[23:])
+
+
+@pytest.mark.parametrize("new,lens", [([4, 1, 2], [700, 3000, 64]), ([64, 1], [300, 900])])
+def test_chunk_in_a_graph(gpu_lib, new, lens):
+    q, cache, table, _ = chunk_inputs(new, lens, 8, 2, 128, 16, True)
+    q, starts = q.cuda(), starts_of(new)
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    replay_equals_eager(lambda: gpu_lib.paged_chunk_attention_fp8(q, *cache, table, lens_, starts, o=o, lse=lse),
+                        [o, lse])
+
+
+def test_lengths_change_between_replays(gpu_lib):
+    """A captured call reads lengths, starts and pages when it runs."""
+    q, cache, table, _ = chunk_inputs([30, 30], [400, 900], 8, 2, 128, 16, False)
+    q = q.cuda()
+    starts, lens_ = starts_of([30, 30]), torch.tensor([400, 900], dtype=torch.int32, device="cuda")
+    o = torch.zeros_like(q)
+    call = lambda: gpu_lib.paged_chunk_attention(q, *cache, table, lens_, starts, o=o)  # noqa: E731
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for first, lens in ((30, [400, 900]), (1, [17, 900]), (59, [399, 1]), (0, [5, 777])):
+        starts.copy_(torch.tensor([0, first, 60], dtype=torch.int32))
+        lens_.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        got = o.clone()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(got, o), (first, lens)
+
+
+def test_binding_refusals(gpu_lib):
+    q, cache, table, _ = chunk_inputs([3, 2], [9, 20], 4, 2, 64, 16, False)
+    q, lens = q.cuda(), torch.tensor([9, 20], dtype=torch.int32, device="cuda")
+    starts = starts_of([3, 2])
+    f = gpu_lib.paged_chunk_attention
+    with pytest.raises(ValueError, match="block_table"):
+        f(q, *cache, table[:1], lens, starts)
+    with pytest.raises(ValueError, match="seq_lens"):
+        f(q, *cache, table, lens[:1], starts)
+    with pytest.raises(TypeError, match="starts"):
+        f(q, *cache, table, lens, starts.long())
+    with pytest.raises(ValueError, match="q:"):
+        f(q[..., :32].contiguous(), *cache, table, lens, starts)
+    with pytest.raises(TypeError, match="k_cache"):
+        gpu_lib.paged_chunk_attention_fp8(q, *cache, cache[0], cache[0], table, lens, starts)
+    for bad in (dict(max_len=10 ** 6), dict(max_len=-1), dict(window=-1), dict(scale=float("inf")), dict(softcap=-1.0)):
+        with pytest.raises(gpu_lib.Fp8LinError):
+            f(q, *cache, table, lens, starts, **bad)
