@@ -523,8 +523,8 @@ fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache
  *
  *   q [T,Hq,D], k, v [T,Hkv,D] bf16  by strides in values (token, head; a head's D
  *                                    values lie together): views of a QKV projection
- *                                    will do.  Strides are multiples of 8, 0 .. 2^36;
- *                                    Hq a multiple of Hkv: query head n reads key
+ *                                    will do.  Strides are multiples of 8, a token's
+ *                                    0 .. 2^24, a head's 0 .. 2^36; Hq a multiple of Hkv: query head n reads key
  *                                    head n / (Hq / Hkv)
  *   starts [B+1] int32               prompt b is rows starts[b] .. starts[b+1] - 1:
  *                                    nondecreasing, 0 .. T (others are clamped: such

@@ -129,14 +129,16 @@ fp8l_status decode(const DecodeArgs &in, int64_t B, int64_t Hq, int64_t Hkv, int
   return finished(e, sc);
 }
 
-constexpr int64_t kMaxStride = int64_t(1) << 36;
+constexpr int64_t kMaxHeadStride = int64_t(1) << 36, kMaxTokenStride = int64_t(1) << 24;  // 16 tokens by 32-bit offsets
 constexpr float kMaxScale = 0x1p100f;
 
 bool bad_scores(float scale, float softcap, int64_t window) {
   return !(std::fabs(scale) <= kMaxScale) || !(softcap >= 0.0f) || std::isinf(softcap) || window < 0;
 }
 
-bool bad_stride(int64_t s) { return s < 0 || s > kMaxStride || s % 8 != 0; }
+bool bad_strides(int64_t token, int64_t head) {
+  return token < 0 || token > kMaxTokenStride || token % 8 != 0 || head < 0 || head > kMaxHeadStride || head % 8 != 0;
+}
 
 // The attention of several tokens: the arguments that both calls have, already checked.
 fp8l_status prompt(PromptArgs a, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
@@ -336,8 +338,8 @@ fp8l_status prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_
                              int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, float scale,
                              float softcap, int64_t window, int causal, uint16_t *o, float *lse, hipStream_t stream) {
   if (bad_cache(Hq, Hkv, D, 1, 16) || bad_tokens(B, T, Hq, Hkv, D) || bad_scores(scale, softcap, window) ||
-      (window > 0 && !causal) || bad_stride(q_token) || bad_stride(q_head) || bad_stride(k_token) ||
-      bad_stride(k_head) || bad_stride(v_token) || bad_stride(v_head))
+      (window > 0 && !causal) || bad_strides(q_token, q_head) || bad_strides(k_token, k_head) ||
+      bad_strides(v_token, v_head))
     return FP8L_ERR_SHAPE;
   if (B == 0 || T == 0) return FP8L_OK;
   if (!q || !k || !v || !starts || !o) return FP8L_ERR_NULL;

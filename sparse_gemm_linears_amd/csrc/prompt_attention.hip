@@ -61,6 +61,13 @@ __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
 
 #define FP8LIN_INLINE __attribute__((always_inline))
 
+// The same value, of which the compiler knows nothing: what is computed from it in a path that is
+// rarely taken is not computed ahead of the loop, where it would hold registers.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 enum class Source { kRows, kCache, kCodes };  // strided bf16 rows, a bf16 cache, an e4m3 cache
 
 // Position of 16-byte chunk c of row r in an LDS row of D values.
@@ -117,6 +124,11 @@ __device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, 
   return true;
 }
 
+// Of two bf16 values, the top bit of each that is an infinity or a NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
 // c tanh(x / c) of each value.  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that would
 // lose a small score's low bits, its power series (2^-26 of it is left out).
 template <int N>
@@ -145,9 +157,11 @@ template <int D, Source SRC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, PromptPlan plan, float *part) {
   constexpr bool kPaged = SRC != Source::kRows, kFp8 = SRC == Source::kCodes;
   constexpr int KT = prompt_tile_keys(D), S = KT / 32, kRow = 2 * D;  // bytes of an LDS row
-  constexpr int kBlockRows = WAVES * kWaveRows, kChunks = D / 8;
+  constexpr int kBlockRows = WAVES * kWaveRows;
   __shared__ __align__(1024) uint8_t lds_k0[KT * kRow], lds_k1[KT * kRow], lds_v0[KT * kRow], lds_v1[KT * kRow];
   __shared__ __align__(16) float lds_s0[kFp8 ? 2 * KT : 1], lds_s1[kFp8 ? 2 * KT : 1];
+  __shared__ __align__(16) uint16_t lds_odd[KT * D / 8];  // of a chunk of eight values, two bits for each
+  __shared__ int lds_any[2];
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), n = lane & 31, h = lane >> 5;
   const int group = a.Hq / a.Hkv;
   const uint32_t self = (uint32_t)plan.first + blockIdx.x, rest = self / (uint32_t)a.Hkv;
@@ -173,6 +187,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
   const int all_low = low_of(last_place);
   const int any_end = a.causal ? last_place + 1 : blk.end, any_low = low_of(first_place);
 
+  // keys from block_low to block_end - 1 are seen by all rows of the block
+  const int block_end = a.causal ? blk.place0 + blk.row0 / group + 1 : blk.end;
+  const int block_low = low_of(blk.place0 + (min(blk.row0 + kBlockRows, blk.rows) - 1) / group);
+  if (threadIdx.x < 2) lds_any[threadIdx.x] = 0;  // (before the first barrier)
+
   v8bf qf[D / 16];
   {
     const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)head * a.q_head + 8 * h;
@@ -191,9 +210,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
   float m = -INFINITY, l = 0.f;
   const float scale = fabsf(a.scale);
 
-  // Copies.  A wave's copy of 64 x 16 bytes covers a few rows, all in one run of 16 keys (which
-  // lies in one page).  Keys that no row sees may hold anything, so their rows repeat
-  // the nearest key that is seen.
+  // Copies.  Keys are taken in runs of 16 (which lie in one page): a wave's copy of 64 x 16
+  // bytes covers a few rows of one run, at an address that the wave shares and offsets of
+  // the lanes that repeat with the runs.
   int64_t found = 0;   // of a cache: lane x holds the line of run x of the next 64 runs
   int found_from = 0;  // key of run 0
   auto look_up = [&](int key0) FP8LIN_INLINE {
@@ -205,56 +224,77 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
       found = ((int64_t)page * a.Hkv + kvh) * a.page_size + (key - p * a.page_size);
     }
   };
-  // line (in a cache) of the run of keys with tile row r of the tile at key0
-  auto run_line = [&](int key0, int r) { return from_lane(found, (key0 - found_from) / 16 + (r >> 4)); };
+  // line (in a cache) or token of the first key of run `run` of the tile at key0
+  auto run_line = [&](int key0, int run) FP8LIN_INLINE -> int64_t {
+    return kPaged ? from_lane(found, (key0 - found_from) / 16 + run) : (int64_t)blk.start + key0 + 16 * run;
+  };
+  constexpr int kBytes = kFp8 ? 1 : 2;  // of a value in memory
+  const int64_t k_line = kPaged ? D * kBytes : a.k_token * 2, v_line = kPaged ? D * kBytes : a.v_token * 2;
+  const char *k_base = static_cast<const char *>(a.k) + (kPaged ? 0 : (int64_t)kvh * a.k_head * 2);
+  const char *v_base = static_cast<const char *>(a.v) + (kPaged ? 0 : (int64_t)kvh * a.v_head * 2);
+  // Rows of a tile that no row of the block sees may hold anything: such rows repeat the nearest
+  // key that is seen.  Row r of the tile at key0 is then row near(r).
+  auto near = [&](int key0, int r) FP8LIN_INLINE { return max(min(r, blk.end - 1 - key0), blk.lowest - key0); };
+  auto whole = [&](int key0) FP8LIN_INLINE { return key0 >= blk.lowest && key0 + KT <= blk.end; };
 
-  constexpr int kCopyRows = 512 / D;  // rows of a wave's copy of bf16 values
+  constexpr int kCopyRows = 1024 / (D * kBytes);  // rows of a wave's copy
+  constexpr int kLanes = 64 / kCopyRows;          // lanes of a row
   constexpr int kCopies = KT / kCopyRows, kCopiesPer = (kCopies + WAVES - 1) / WAVES;
-  auto copy_tile = [&](int key0, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
-    const int last = blk.end - 1 - key0, lowest = blk.lowest - key0;  // tile rows of the keys that are seen
+  // copy i of a wave covers rows copy_row(i) on; rows are alike modulo 16, so a few offsets serve all
+  constexpr int kStep = kCopyRows * WAVES;
+  constexpr int kKinds = kStep % 16 == 0 ? 1 : 16 / kStep < kCopiesPer ? 16 / kStep : kCopiesPer;
+  auto copy_row = [&](int i) FP8LIN_INLINE { return i * kStep + wave * kCopyRows; };
+  uint32_t k_off[kKinds], v_off[kKinds];
+  auto offsets = [&](int r, int c, int src, uint32_t &ko, uint32_t &vo) FP8LIN_INLINE {
+    ko = (uint32_t)((src & 15) * (int)k_line + 16 * (kFp8 ? c : key_swizzle<D>(r, c)));
+    vo = (uint32_t)((src & 15) * (int)v_line + 16 * (kFp8 ? c : value_swizzle<D>(r, c)));
+  };
 #pragma unroll
-    for (int i = 0; i < kCopiesPer; i++) {
-      const int r0 = (i * WAVES + wave) * kCopyRows;
-      if (kCopies % WAVES != 0 && r0 >= KT) break;
-      const int r = r0 + lane / kChunks, c = lane % kChunks;
-      const int src = max(min(r, last), lowest);
-      const int kc = key_swizzle<D>(r, c) * 8, vc = value_swizzle<D>(r, c) * 8;
-      const uint16_t *kp, *vp;
-      if constexpr (kPaged) {
-        const int64_t line = run_line(key0, min(r0, last)) * D;
-        kp = static_cast<const uint16_t *>(a.k) + line + ((src & 15) * D + kc);
-        vp = static_cast<const uint16_t *>(a.v) + line + ((src & 15) * D + vc);
-      } else {
-        const int64_t t = blk.start + key0 + src;
-        kp = static_cast<const uint16_t *>(a.k) + t * a.k_token + (int64_t)kvh * a.k_head + kc;
-        vp = static_cast<const uint16_t *>(a.v) + t * a.v_token + (int64_t)kvh * a.v_head + vc;
-      }
-      copy16_global_to_lds(kp, lk + r0 * kRow);
-      copy16_global_to_lds(vp, lv + r0 * kRow);
+  for (int i = 0; i < kKinds; i++) {
+    const int r = copy_row(i) + lane / kLanes;
+    offsets(r, lane % kLanes, r, k_off[i], v_off[i]);
+  }
+  // e4m3 codes go through registers: 16 codes of a lane become 32 bytes of bf16
+  uint4 raw_k[kFp8 ? kCopiesPer : 1], raw_v[kFp8 ? kCopiesPer : 1];
+  float raw_s[2];
+  auto copy_rows = [&](int i, int64_t line, uint32_t ko, uint32_t vo, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
+    const char *kp = k_base + line * k_line + ko, *vp = v_base + line * v_line + vo;
+    if constexpr (kFp8) {
+      raw_k[i] = *reinterpret_cast<const uint4 *>(kp);
+      raw_v[i] = *reinterpret_cast<const uint4 *>(vp);
+    } else {
+      copy16_global_to_lds(kp, lk + copy_row(i) * kRow);
+      copy16_global_to_lds(vp, lv + copy_row(i) * kRow);
     }
   };
-  // e4m3 codes go through registers: 16 codes of a lane become 32 bytes of bf16
-  constexpr int kCodeRows = 1024 / D, kLoads = KT / kCodeRows, kLoadsPer = (kLoads + WAVES - 1) / WAVES;
-  uint4 raw_k[kFp8 ? kLoadsPer : 1], raw_v[kFp8 ? kLoadsPer : 1];
-  float raw_s[kFp8 && WAVES == 1 ? 2 : 1];
-  auto load_codes = [&](int key0) FP8LIN_INLINE {
-    const int last = blk.end - 1 - key0, lowest = blk.lowest - key0;
-#pragma unroll
-    for (int i = 0; i < kLoadsPer; i++) {
-      const int r0 = (i * WAVES + wave) * kCodeRows;
-      if (kLoads % WAVES != 0 && r0 >= KT) break;
-      const int r = r0 + lane / (D / 16), c = lane % (D / 16);
-      const int src = max(min(r, last), lowest);
-      const int64_t at = run_line(key0, min(r0, last)) * D + ((src & 15) * D + 16 * c);
-      raw_k[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.k) + at);
-      raw_v[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.v) + at);
+  auto fetch = [&](int t, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
+    const int key0 = blk.begin + t * KT;
+    if constexpr (kPaged) {
+      if (t == tile0 || key0 + KT > found_from + 1024) look_up(key0);
     }
-    // the scales: wave 0 the keys', the last wave the values'
-    if (wave == 0 || wave == WAVES - 1) {
-      const int src = max(min(lane & (KT - 1), last), lowest);
-      const int64_t at = __shfl(found, (key0 - found_from) / 16 + (src >> 4), 64) + (src & 15);
-      raw_s[0] = (wave == 0 ? a.k_scale : a.v_scale)[at];
-      if constexpr (WAVES == 1) raw_s[kFp8 ? 1 : 0] = a.v_scale[at];
+    if (whole(key0)) {
+#pragma unroll
+      for (int i = 0; i < kCopiesPer; i++) {
+        if (kCopies % WAVES != 0 && copy_row(i) >= KT) break;
+        copy_rows(i, run_line(key0, copy_row(i) >> 4), k_off[i % kKinds], v_off[i % kKinds], lk, lv);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCopiesPer; i++) {
+        if (kCopies % WAVES != 0 && copy_row(i) >= KT) break;
+        const int self = opaque(lane), r = copy_row(i) + self / kLanes;
+        uint32_t ko, vo;
+        offsets(r, self % kLanes, near(key0, r), ko, vo);
+        copy_rows(i, run_line(key0, uniform(near(key0, copy_row(i))) >> 4), ko, vo, lk, lv);
+      }
+    }
+    if constexpr (kFp8) {  // the scales: the first wave those of the keys, the last those of the values
+      if (wave == 0 || wave == WAVES - 1) {
+        const int src = near(key0, lane & (KT - 1));
+        const int64_t at = __shfl(found, (key0 - found_from) / 16 + (src >> 4), 64) + (src & 15);
+        if (wave == 0) raw_s[0] = a.k_scale[at];
+        if (wave == WAVES - 1) raw_s[1] = a.v_scale[at];
+      }
     }
   };
   auto store_codes = [&](uint8_t *lk, uint8_t *lv, float *ls) FP8LIN_INLINE {
@@ -270,15 +310,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
       *reinterpret_cast<uint4 *>(row_at + 16 * c1) = make_uint4(b[4], b[5], b[6], b[7]);
     };
 #pragma unroll
-    for (int i = 0; i < kLoadsPer; i++) {
-      const int r0 = (i * WAVES + wave) * kCodeRows;
-      if (kLoads % WAVES != 0 && r0 >= KT) break;
-      const int r = r0 + lane / (D / 16), c = 2 * (lane % (D / 16));
+    for (int i = 0; i < kCopiesPer; i++) {
+      if (kCopies % WAVES != 0 && copy_row(i) >= KT) break;
+      const int r = copy_row(i) + lane / kLanes, c = 2 * (lane % kLanes);
       put(raw_k[i], lk + r * kRow, key_swizzle<D>(r, c), key_swizzle<D>(r, c + 1));
       put(raw_v[i], lv + r * kRow, value_swizzle<D>(r, c), value_swizzle<D>(r, c + 1));
     }
     if (wave == 0 && lane < KT) ls[lane] = raw_s[0];
-    if (wave == WAVES - 1 && lane < KT) ls[KT + lane] = raw_s[kFp8 && WAVES == 1 ? 1 : 0];
+    if (wave == WAVES - 1 && lane < KT) ls[KT + lane] = raw_s[1];
   };
 
   // Reads of a tile's fragments.
@@ -295,15 +334,29 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     return __builtin_bit_cast(v8bf, (v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}));
   };
 
-  auto use_tile = [&](int key0, uint8_t *lk, uint8_t *lv, const float *ls) FP8LIN_INLINE {
+  // edge: some row of the wave does not see some key of the tile; odd: lds_odd has values
+  // that were taken out of the tile.
+  auto use_tile = [&](int key0, uint8_t *lk, uint8_t *lv, const float *ls, bool edge, bool odd) FP8LIN_INLINE {
+    // Fragments are read one step ahead of the products that take them, and no earlier: the
+    // compiler would fill the registers with them.
     v16f sc[S];
+    v8bf kf[2][S];
 #pragma unroll
     for (int sub = 0; sub < S; sub++) {
 #pragma unroll
       for (int j = 0; j < 16; j++) sc[sub][j] = 0.f;
+      kf[0][sub] = key_frag(lk, sub, 0);
+    }
 #pragma unroll
-      for (int s = 0; s < D / 16; s++)
-        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(lk, sub, s), qf[s], sc[sub], 0, 0, 0);
+    for (int s = 0; s < D / 16; s++) {
+      if (s + 1 < D / 16) {
+#pragma unroll
+        for (int sub = 0; sub < S; sub++) kf[(s + 1) & 1][sub] = key_frag(lk, sub, s + 1);
+      }
+#pragma unroll
+      for (int sub = 0; sub < S; sub++)
+        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s & 1][sub], qf[s], sc[sub], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
     float x[16 * S];
 #pragma unroll
@@ -325,10 +378,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
       if (a.softcap > 0.f) cap_scores(x, a.softcap);
       rate = kLog2e;
     }
-    const bool masked = key0 + KT > all_end || key0 < all_low;
     const int live_end = seen_end - key0 - 4 * h, live_low = seen_low - key0 - 4 * h;
     auto live = [&](int j) { return 8 * (j >> 2) + (j & 3) < live_end && 8 * (j >> 2) + (j & 3) >= live_low; };
-    if (masked) {
+    if (edge) {
 #pragma unroll
       for (int j = 0; j < 16 * S; j++) x[j] = live(j) ? x[j] : -INFINITY;
     }
@@ -365,7 +417,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
         x[4 * j + 2] *= vs.z;
         x[4 * j + 3] *= vs.w;
       }
-      if (masked) {  // a scale that is not finite belongs to no row that does not see its key
+      if (edge) {  // a scale that is not finite belongs to no row that does not see its key
 #pragma unroll
         for (int j = 0; j < 16 * S; j++) x[j] = live(j) ? x[j] : 0.f;
       }
@@ -375,61 +427,77 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     for (int s = 0; s < 2 * S; s++)
       p[s] = as_bf16x8(pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
                        pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7]));
-    if (masked) {
-      // 0 times an infinity or a NaN is a NaN: a value that is not finite must not reach
-      // rows that do not see its key.
-      uint32_t odd = 0;
-      for (int i = lane; i < KT * kRow / 16; i += 64) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(lv + 16 * i);
-        odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-               ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-      }
-      if (__builtin_expect(__any((odd & 0x80008000u) != 0), 0)) {
-        // one key at a time, added where it is seen
+    v8bf vf[2];
+    vf[0] = value_frag(lv, 0, 0);
 #pragma unroll
-        for (int s = 0; s < 2 * S; s++) {
-          for (int key = 0; key < 16; key++) {
-            const int at = 16 * s + key - 4 * h;
-            const bool seen = at < live_end && at >= live_low;
-            const uint32_t half = key & 1 ? 0xFFFF0000u : 0xFFFFu;
-            const int word = h == (key >> 2 & 1) ? (key & 3) / 2 + 2 * (key >> 3) : -1;
-            auto only = [&](const v8bf &f) FP8LIN_INLINE {
-              const v4u w = __builtin_bit_cast(v4u, f);
-              return as_bf16x8(word == 0 ? w[0] & half : 0, word == 1 ? w[1] & half : 0, word == 2 ? w[2] & half : 0,
-                               word == 3 ? w[3] & half : 0);
-            };
-            const v8bf weight = only(p[s]);
+    for (int i = 0; i < D / 32 * 2 * S; i++) {
+      constexpr int kDb = D / 32;
+      if (i + 1 < kDb * 2 * S) vf[(i + 1) & 1] = value_frag(lv, (i + 1) % kDb, (i + 1) / kDb);
+      o[i % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i & 1], p[i / kDb], o[i % kDb], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (__builtin_expect(odd, 0)) {
+      // The rows that see such a value get what a sum with it is.
+      uint32_t flags[D / 16] = {};  // of the values of the keys that the row sees
+#pragma unroll 1
+      for (int key = max(0, seen_low - key0); key < min(KT, seen_end - key0); key++) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(lds_odd + key * (D / 8));
 #pragma unroll
-            for (int db = 0; db < D / 32; db++) {
-              v16f sum;
-#pragma unroll
-              for (int j = 0; j < 16; j++) sum[j] = 0.f;
-              sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(only(value_frag(lv, db, s)), weight, sum, 0, 0, 0);
-#pragma unroll
-              for (int j = 0; j < 16; j++) o[db][j] = seen ? o[db][j] + sum[j] : o[db][j];
-            }
-          }
+        for (int w = 0; w < D / 64; w++) {
+          const uint4 f = at[w];
+          flags[4 * w] |= f.x;
+          flags[4 * w + 1] |= f.y;
+          flags[4 * w + 2] |= f.z;
+          flags[4 * w + 3] |= f.w;
         }
-        return;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; i++) {
+        const uint32_t f = flags[i / 2] >> (16 * (i & 1) + 8 * h);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          o[i / 4][4 * (i % 4) + j] += (f >> 2 * j & 1 ? INFINITY : 0.f) - (f >> 2 * j & 2 ? INFINITY : 0.f);
       }
     }
+  };
+  // 0 times an infinity or a NaN is a NaN, and such a value must not reach rows that do not see
+  // its key: they are taken out of a tile of values and noted in lds_odd.
+  auto take_odd = [&](uint8_t *lv, int parity) FP8LIN_INLINE -> bool {
+    bool mine = false;
+    const int self = opaque(threadIdx.x);
+    for (int i = self; i < KT * D / 8; i += 64 * WAVES) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(lv + 16 * i);
+      mine |= (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) != 0;
+    }
+    if (mine) lds_any[parity] = 1;
+    __syncthreads();
+    const bool any = lds_any[parity] != 0;
+    if (__builtin_expect(!any, 1)) return false;
+    for (int i = self; i < KT * D / 8; i += 64 * WAVES) {
+      uint4 *at = reinterpret_cast<uint4 *>(lv + 16 * i);
+      const uint4 x = *at;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t kept[4], flags = 0;
 #pragma unroll
-    for (int db = 0; db < D / 32; db++)
+      for (int j = 0; j < 4; j++) {
+        kept[j] = w[j];
 #pragma unroll
-      for (int s = 0; s < 2 * S; s++)
-        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value_frag(lv, db, s), p[s], o[db], 0, 0, 0);
+        for (int e = 0; e < 2; e++) {
+          const uint32_t v = w[j] >> 16 * e & 0xFFFFu;
+          if ((v & 0x7F80u) != 0x7F80u) continue;
+          kept[j] &= ~(0xFFFFu << 16 * e);
+          flags |= (v & 0x7Fu ? 3u : v >> 15 ? 2u : 1u) << (4 * j + 2 * e);
+        }
+      }
+      const int r = i / (D / 8), c = i % (D / 8);  // position c holds chunk value_swizzle(r, c): it is its own inverse
+      lds_odd[r * (D / 8) + value_swizzle<D>(r, c)] = (uint16_t)flags;
+      *at = make_uint4(kept[0], kept[1], kept[2], kept[3]);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) lds_any[parity] = 0;
+    return true;
   };
 
-  auto fetch = [&](int t, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
-    const int key0 = blk.begin + t * KT;
-    if constexpr (kPaged) {
-      if (t == tile0 || key0 + KT > found_from + 1024) look_up(key0);
-    }
-    if constexpr (kFp8)
-      load_codes(key0);
-    else
-      copy_tile(key0, lk, lv);
-  };
   auto step = [&](int t, auto stage) FP8LIN_INLINE {
     constexpr bool kOdd = decltype(stage)::value;
     uint8_t *lk = kOdd ? lds_k1 : lds_k0, *lv = kOdd ? lds_v1 : lds_v0;
@@ -441,7 +509,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     __syncthreads();
     if (t + 1 < tile_end) fetch(t + 1, kOdd ? lds_k0 : lds_k1, kOdd ? lds_v0 : lds_v1);
     const int key0 = blk.begin + t * KT;
-    if (working && key0 < any_end && key0 + KT > any_low) use_tile(key0, lk, lv, ls);
+    bool odd = false;
+    if (key0 + KT > block_end || key0 < block_low) odd = take_odd(lv, kOdd);
+    if (!working || key0 >= any_end || key0 + KT <= any_low) return;
+    use_tile(key0, lk, lv, ls, key0 + KT > all_end || key0 < all_low, odd);
   };
   if (tile0 < tile_end) {
     fetch(tile0, lds_k0, lds_v0);
