@@ -152,6 +152,8 @@ fp8l_status prompt(PromptArgs a, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, 
   a.window = (int)(window < kMaxTokens ? window : kMaxTokens);
   // a smaller cap has no reciprocal, and leaves scores that no exponential tells from 0 either
   if (a.softcap > 0.0f && a.softcap < 1e-30f) a.softcap = 1e-30f;
+  // scores of a scale of 0 are 0 under any cap; without one 0 times the -infinity of a hidden key would be a NaN
+  if (a.scale == 0.0f && a.softcap == 0.0f) a.softcap = 1.0f;
   CallScratch sc;
   if (hipError_t e = sc.acquire(prompt_partial_bytes(a, device_cu_count()), 0, stream)) return launched(e);
   const hipError_t e = launch_prompt_attention(a, sc.partials(), stream);

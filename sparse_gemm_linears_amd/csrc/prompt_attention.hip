@@ -68,6 +68,15 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
+// Neither loads nor anything else is moved past this place.
+__device__ __forceinline__ void step_ends() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A barrier for LDS alone: unlike __syncthreads it does not wait for the copies under way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 enum class Source { kRows, kCache, kCodes };  // strided bf16 rows, a bf16 cache, an e4m3 cache
 
 // Position of 16-byte chunk c of row r in an LDS row of D values.
@@ -93,14 +102,13 @@ struct Block {
 __device__ __forceinline__ int start_of(const PromptArgs &a, int b) { return min(max(a.starts[b], 0), a.T); }
 
 // Finds block `number` of the batch; false if the number is not used.
-__device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, int block_rows, int tile_keys,
-                                           Block &k) {
+__device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, int tile, Block &k) {
   const int lane = threadIdx.x & 63, group = a.Hq / a.Hkv;
   // the last sequence whose numbers start at `number` or before, 64 candidates at a time
   int low = 0, high = a.B;
   while (high - low > 1 || low == 0) {
     const int step = (high - low + 63) / 64, b = low + lane * step;
-    const bool before = b < high && first_block(start_of(a, min(b, a.B - 1)), b, group, block_rows) <= number;
+    const bool before = b < high && first_block(start_of(a, min(b, a.B - 1)), b, group) <= number;
     const int count = __popcll(__ballot(before));
     if (count == 0) return false;
     low += (count - 1) * step;
@@ -110,17 +118,17 @@ __device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, 
   k.b = uniform(low);
   k.start = uniform(start_of(a, k.b));
   k.tokens = uniform(start_of(a, k.b + 1)) - k.start;
-  const int64_t row0 = (number - first_block(k.start, k.b, group, block_rows)) * block_rows;
+  const int64_t row0 = (number - first_block(k.start, k.b, group)) * kBlockRows;
   if (k.tokens <= 0 || row0 < 0 || row0 >= (int64_t)k.tokens * group) return false;
-  k.row0 = (int)row0;
+  k.row0 = uniform((int)row0);
   k.rows = k.tokens * group;
-  const int first = k.row0 / group, last = min(k.row0 + block_rows, k.rows) - 1;
+  const int first = k.row0 / group, last = min(k.row0 + kBlockRows, k.rows) - 1;
   const int keys = a.block_table ? uniform(min(max(a.seq_lens[k.b], 0), a.max_len)) : k.tokens;
   k.place0 = keys - k.tokens;
   k.end = a.causal ? max(0, k.place0 + last / group + 1) : keys;
   k.lowest = a.window > 0 ? max(0, k.place0 + first - a.window + 1) : 0;
   k.begin = k.lowest & ~15;
-  k.tiles = (max(0, k.end - k.begin) + tile_keys - 1) / tile_keys;
+  k.tiles = (max(0, k.end - k.begin) + tile - 1) / tile;
   return true;
 }
 
@@ -153,11 +161,10 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float cap) {
   }
 }
 
-template <int D, Source SRC, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, PromptPlan plan, float *part) {
+template <int D, Source SRC, bool CAP>
+__global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs a, PromptPlan plan, float *part) {
   constexpr bool kPaged = SRC != Source::kRows, kFp8 = SRC == Source::kCodes;
-  constexpr int KT = prompt_tile_keys(D), S = KT / 32, kRow = 2 * D;  // bytes of an LDS row
-  constexpr int kBlockRows = WAVES * kWaveRows;
+  constexpr int KT = tile_keys(D), WAVES = kBlockWaves, kRow = 2 * D;  // bytes of an LDS row
   __shared__ __align__(1024) uint8_t lds_k0[KT * kRow], lds_k1[KT * kRow], lds_v0[KT * kRow], lds_v1[KT * kRow];
   __shared__ __align__(16) float lds_s0[kFp8 ? 2 * KT : 1], lds_s1[kFp8 ? 2 * KT : 1];
   __shared__ __align__(16) uint16_t lds_odd[KT * D / 8];  // of a chunk of eight values, two bits for each
@@ -169,14 +176,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
   const int split = (int)(rest % (uint32_t)plan.splits);
   const int64_t number = plan.blocks - 1 - (int)(rest / (uint32_t)plan.splits);  // a sequence's longest rows first
   Block blk;
-  if (!find_block(a, number, kBlockRows, KT, blk)) return;
+  if (!find_block(a, number, KT, blk)) return;
   const int tile0 = split * plan.per, tile_end = min(blk.tiles, tile0 + plan.per);
   if (split > 0 && tile0 >= blk.tiles) return;
 
+  // Blocks of more than 64 rows: a wave takes 32 of them and all keys of a tile.  Smaller ones: two
+  // waves share 32 rows and take 32 keys of a tile each, so that half the waves are not idle.
+  const bool shared = KT == 64 && min(kBlockRows, blk.rows - blk.row0) <= 2 * kWaveRows;
+  const int half = shared ? wave & 1 : 0;  // of the tile's keys
   // the wave's rows; rows past the last one repeat it and are not stored
-  const int wave_row = blk.row0 + wave * kWaveRows;
+  const int wave_row = blk.row0 + (shared ? wave >> 1 : wave) * kWaveRows;
   const bool working = wave_row < blk.rows;
-  const int row = min(wave_row + n, blk.rows - 1), token = row / group, head = kvh * group + row % group;
+  const int row = min(wave_row + n, blk.rows - 1), token = row / group;
   auto low_of = [&](int place) { return a.window > 0 ? place - a.window + 1 : 0; };
   const int place = blk.place0 + token;
   const int seen_end = a.causal ? place + 1 : blk.end, seen_low = low_of(place);
@@ -194,8 +205,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
 
   v8bf qf[D / 16];
   {
-    const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)head * a.q_head + 8 * h;
-    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;  // the weights' exponents grow with the scores
+    const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head + 8 * h;
+    // the weights' exponents grow with the scores: a negative scale turns the queries over
+    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int s = 0; s < D / 16; s++) {
       const uint4 raw = *reinterpret_cast<const uint4 *>(src + 16 * s);
@@ -309,10 +321,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
       *reinterpret_cast<uint4 *>(row_at + 16 * c0) = make_uint4(b[0], b[1], b[2], b[3]);
       *reinterpret_cast<uint4 *>(row_at + 16 * c1) = make_uint4(b[4], b[5], b[6], b[7]);
     };
+    const int self = opaque(lane);
 #pragma unroll
     for (int i = 0; i < kCopiesPer; i++) {
       if (kCopies % WAVES != 0 && copy_row(i) >= KT) break;
-      const int r = copy_row(i) + lane / kLanes, c = 2 * (lane % kLanes);
+      const int r = copy_row(i) + self / kLanes, c = 2 * (self % kLanes);
       put(raw_k[i], lk + r * kRow, key_swizzle<D>(r, c), key_swizzle<D>(r, c + 1));
       put(raw_v[i], lv + r * kRow, value_swizzle<D>(r, c), value_swizzle<D>(r, c + 1));
     }
@@ -320,43 +333,52 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     if (wave == WAVES - 1 && lane < KT) ls[KT + lane] = raw_s[1];
   };
 
-  // Reads of a tile's fragments.
-  auto key_frag = [&](const uint8_t *lk, int sub, int s) FP8LIN_INLINE {
-    const uint4 raw = *reinterpret_cast<const uint4 *>(lk + (32 * sub + n) * kRow + 16 * key_swizzle<D>(n, 2 * s + h));
+  // Reads of a tile's fragments, from the lane's place in it: steps and value blocks change bits
+  // of the place that nothing else has.
+  const int key_at = (32 * half + n) * kRow + 16 * key_swizzle<D>(n, h);
+  const int value_r = 4 * h + (lane & 15) / 4;
+  const int value_at = (32 * half + value_r) * kRow + 16 * value_swizzle<D>(value_r, 2 * (lane >> 4 & 1) + (lane & 3) / 2) +
+                       8 * (lane & 1);
+  auto key_frag = [&](const uint8_t *lk, int at, int sub, int s) FP8LIN_INLINE {
+    const uint4 raw = *reinterpret_cast<const uint4 *>(lk + (at ^ 32 * s) + 32 * sub * kRow);
     return as_bf16x8(raw.x, raw.y, raw.z, raw.w);
   };
-  auto value_frag = [&](uint8_t *lv, int db, int step) FP8LIN_INLINE {  // values 32 db .. + 31 of keys 16 step .. + 15
-    const int r = 4 * h + (lane & 15) / 4, c = 4 * db + 2 * (lane >> 4 & 1) + (lane & 3) / 2;
-    uint8_t *at = lv + (16 * step + r) * kRow + 16 * value_swizzle<D>(r, c) + 8 * (lane & 1);
-    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 8 * kRow));
+  auto value_frag = [&](uint8_t *lv, int at, int db, int step) FP8LIN_INLINE {  // values 32 db .. of keys 16 step ..
+    uint8_t *p = lv + (at ^ 64 * db) + 16 * step * kRow;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 8 * kRow));
     typedef short v8s __attribute__((ext_vector_type(8)));
     return __builtin_bit_cast(v8bf, (v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}));
   };
 
   // edge: some row of the wave does not see some key of the tile; odd: lds_odd has values
   // that were taken out of the tile.
-  auto use_tile = [&](int key0, uint8_t *lk, uint8_t *lv, const float *ls, bool edge, bool odd) FP8LIN_INLINE {
-    // Fragments are read one step ahead of the products that take them, and no earlier: the
+  auto use_tile = [&](auto subs, int key0, uint8_t *lk, uint8_t *lv, const float *ls, bool edge, bool odd) FP8LIN_INLINE {
+    constexpr int S = decltype(subs)::value;
+    // Fragments are read a few steps ahead of the products that take them, and no earlier: the
     // compiler would fill the registers with them.
+    constexpr int kKeyRing = S == 2 ? 3 : 4, kSteps = D / 16;
+    const int ka = opaque(key_at);
     v16f sc[S];
-    v8bf kf[2][S];
+    v8bf kf[kKeyRing][S];
+    auto read_keys = [&](int s) FP8LIN_INLINE {
 #pragma unroll
-    for (int sub = 0; sub < S; sub++) {
+      for (int sub = 0; sub < S; sub++) kf[s % kKeyRing][sub] = key_frag(lk, ka, sub, s);
+    };
+#pragma unroll
+    for (int s = 0; s + 1 < kKeyRing; s++) read_keys(s);
+#pragma unroll
+    for (int sub = 0; sub < S; sub++)
 #pragma unroll
       for (int j = 0; j < 16; j++) sc[sub][j] = 0.f;
-      kf[0][sub] = key_frag(lk, sub, 0);
-    }
 #pragma unroll
-    for (int s = 0; s < D / 16; s++) {
-      if (s + 1 < D / 16) {
-#pragma unroll
-        for (int sub = 0; sub < S; sub++) kf[(s + 1) & 1][sub] = key_frag(lk, sub, s + 1);
-      }
+    for (int s = 0; s < kSteps; s++) {
+      if (s + kKeyRing - 1 < kSteps) read_keys(s + kKeyRing - 1);
+      step_ends();
 #pragma unroll
       for (int sub = 0; sub < S; sub++)
-        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s & 1][sub], qf[s], sc[sub], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % kKeyRing][sub], qf[s], sc[sub], 0, 0, 0);
+      step_ends();
     }
     float x[16 * S];
 #pragma unroll
@@ -364,6 +386,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     if constexpr (kFp8) {
 #pragma unroll
       for (int j = 0; j < 4 * S; j++) {
+        if (j % 4 == 0) __builtin_amdgcn_sched_barrier(0);
         const float4 ks = *reinterpret_cast<const float4 *>(ls + 8 * j + 4 * h);
         x[4 * j] *= ks.x;
         x[4 * j + 1] *= ks.y;
@@ -371,13 +394,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
         x[4 * j + 3] *= ks.w;
       }
     }
-    float rate = scale * kLog2e;  // of the exponents in units of x
-    if (a.softcap > 0.f || scale == 0.f) {  // (0 times the -infinity of a hidden key would be a NaN)
+    if constexpr (CAP) {
 #pragma unroll
       for (int j = 0; j < 16 * S; j++) x[j] *= scale;
-      if (a.softcap > 0.f) cap_scores(x, a.softcap);
-      rate = kLog2e;
+      cap_scores(x, a.softcap);
     }
+    const float rate = CAP ? kLog2e : scale * kLog2e;  // of the exponents in units of x
     const int live_end = seen_end - key0 - 4 * h, live_low = seen_low - key0 - 4 * h;
     auto live = [&](int j) { return 8 * (j >> 2) + (j & 3) < live_end && 8 * (j >> 2) + (j & 3) >= live_low; };
     if (edge) {
@@ -399,6 +421,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
 #pragma unroll
       for (int i = 0; i < D / 32; i++) o[i] *= shrink;
     }
+    constexpr int kDb = D / 32, kProducts = kDb * 2 * S, kValueRing = 4;
+    const int va = opaque(value_at);
+    v8bf vf[kValueRing];
+    auto read_values = [&](int i) FP8LIN_INLINE { vf[i % kValueRing] = value_frag(lv, va, i % kDb, i / kDb); };
+#pragma unroll
+    for (int i = 0; i + 1 < kValueRing; i++) read_values(i);
+    step_ends();
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < 16 * S; j++) x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], rate, -base));
@@ -411,6 +440,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     if constexpr (kFp8) {
 #pragma unroll
       for (int j = 0; j < 4 * S; j++) {
+        if (j % 4 == 0) __builtin_amdgcn_sched_barrier(0);
         const float4 vs = *reinterpret_cast<const float4 *>(ls + KT + 8 * j + 4 * h);
         x[4 * j] *= vs.x;
         x[4 * j + 1] *= vs.y;
@@ -427,21 +457,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     for (int s = 0; s < 2 * S; s++)
       p[s] = as_bf16x8(pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
                        pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7]));
-    v8bf vf[2];
-    vf[0] = value_frag(lv, 0, 0);
 #pragma unroll
-    for (int i = 0; i < D / 32 * 2 * S; i++) {
-      constexpr int kDb = D / 32;
-      if (i + 1 < kDb * 2 * S) vf[(i + 1) & 1] = value_frag(lv, (i + 1) % kDb, (i + 1) / kDb);
-      o[i % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i & 1], p[i / kDb], o[i % kDb], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < kProducts; i++) {
+      if (i + kValueRing - 1 < kProducts) read_values(i + kValueRing - 1);
+      step_ends();
+      o[i % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % kValueRing], p[i / kDb], o[i % kDb], 0, 0, 0);
+      step_ends();
     }
     if (__builtin_expect(odd, 0)) {
       // The rows that see such a value get what a sum with it is.
       uint32_t flags[D / 16] = {};  // of the values of the keys that the row sees
 #pragma unroll 1
-      for (int key = max(0, seen_low - key0); key < min(KT, seen_end - key0); key++) {
-        const uint4 *at = reinterpret_cast<const uint4 *>(lds_odd + key * (D / 8));
+      for (int key = max(0, seen_low - key0); key < min(32 * S, seen_end - key0); key++) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(lds_odd + (key + 32 * half) * (D / 8));
 #pragma unroll
         for (int w = 0; w < D / 64; w++) {
           const uint4 f = at[w];
@@ -470,8 +498,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
       mine |= (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) != 0;
     }
     if (mine) lds_any[parity] = 1;
-    __syncthreads();
-    const bool any = lds_any[parity] != 0;
+    lds_barrier();
+    const bool any = uniform(lds_any[parity]) != 0;
     if (__builtin_expect(!any, 1)) return false;
     for (int i = self; i < KT * D / 8; i += 64 * WAVES) {
       uint4 *at = reinterpret_cast<uint4 *>(lv + 16 * i);
@@ -493,39 +521,81 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
       lds_odd[r * (D / 8) + value_swizzle<D>(r, c)] = (uint16_t)flags;
       *at = make_uint4(kept[0], kept[1], kept[2], kept[3]);
     }
-    __syncthreads();
+    lds_barrier();
     if (threadIdx.x == 0) lds_any[parity] = 0;
     return true;
   };
 
-  auto step = [&](int t, auto stage) FP8LIN_INLINE {
-    constexpr bool kOdd = decltype(stage)::value;
-    uint8_t *lk = kOdd ? lds_k1 : lds_k0, *lv = kOdd ? lds_v1 : lds_v0;
-    float *ls = kOdd ? lds_s1 : lds_s0;
-    if constexpr (kFp8)
-      store_codes(lk, lv, ls);
-    else
-      wait_global_loads();
-    __syncthreads();
-    if (t + 1 < tile_end) fetch(t + 1, kOdd ? lds_k0 : lds_k1, kOdd ? lds_v0 : lds_v1);
-    const int key0 = blk.begin + t * KT;
-    bool odd = false;
-    if (key0 + KT > block_end || key0 < block_low) odd = take_odd(lv, kOdd);
-    if (!working || key0 >= any_end || key0 + KT <= any_low) return;
-    use_tile(key0, lk, lv, ls, key0 + KT > all_end || key0 < all_low, odd);
-  };
-  if (tile0 < tile_end) {
-    fetch(tile0, lds_k0, lds_v0);
+  // subs: sets of 32 keys of a tile that the wave takes
+  auto all_tiles = [&](auto subs) FP8LIN_INLINE {
+    constexpr int kMine = 32 * decltype(subs)::value;
+    auto step = [&](int t, auto stage) FP8LIN_INLINE {
+      constexpr bool kOdd = decltype(stage)::value;
+      uint8_t *lk = kOdd ? lds_k1 : lds_k0, *lv = kOdd ? lds_v1 : lds_v0;
+      float *ls = kOdd ? lds_s1 : lds_s0;
+      if constexpr (kFp8)
+        store_codes(lk, lv, ls);
+      else
+        wait_global_loads();
+      __syncthreads();
+      if (t + 1 < tile_end) fetch(t + 1, kOdd ? lds_k0 : lds_k1, kOdd ? lds_v0 : lds_v1);
+      const int key0 = blk.begin + t * KT, mine = key0 + 32 * half;
+      bool odd = false;
+      if (key0 + KT > block_end || key0 < block_low) odd = take_odd(lv, kOdd);
+      if (working && mine < any_end && mine + kMine > any_low)
+        use_tile(subs, mine, lk, lv, ls + 32 * half, mine + kMine > all_end || mine < all_low, odd);
+    };
+    if (tile0 < tile_end) fetch(tile0, lds_k0, lds_v0);
     for (int t = tile0; t < tile_end; t += 2) {
       step(t, std::false_type{});
       if (t + 1 < tile_end) step(t + 1, std::true_type{});
     }
+  };
+  if constexpr (KT == 64) {
+    if (shared)
+      all_tiles(std::integral_constant<int, 1>{});
+    else
+      all_tiles(std::integral_constant<int, 2>{});
+  } else {
+    all_tiles(std::integral_constant<int, 1>{});
   }
 
+  if (shared) {
+    // the second wave of a pair hands its state to the first, lane by lane
+    __syncthreads();
+    float *box = reinterpret_cast<float *>(wave < 2 ? lds_k0 : lds_k1);
+    float *box_ml = reinterpret_cast<float *>(wave < 2 ? lds_v0 : lds_v1);
+    if (half == 1 && working) {
+#pragma unroll
+      for (int i = 0; i < D / 8; i++)
+        *reinterpret_cast<float4 *>(box + 256 * i + 4 * lane) =
+            make_float4(o[i / 4][4 * (i % 4)], o[i / 4][4 * (i % 4) + 1], o[i / 4][4 * (i % 4) + 2],
+                        o[i / 4][4 * (i % 4) + 3]);
+      box_ml[lane] = m;
+      box_ml[64 + lane] = l;
+    }
+    __syncthreads();
+    if (half == 1) return;
+    const float m2 = box_ml[lane], top = fmaxf(m, m2);
+    const float f1 = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
+    const float f2 = m2 == top ? 1.f : __builtin_amdgcn_exp2f(m2 - top);
+    m = top;
+    l = l * f1 + box_ml[64 + lane] * f2;
+#pragma unroll
+    for (int i = 0; i < D / 8; i++) {
+      const float4 x = *reinterpret_cast<const float4 *>(box + 256 * i + 4 * lane);
+      float *mine = reinterpret_cast<float *>(&o[i / 4]) + 4 * (i % 4);
+      mine[0] = mine[0] * f1 + x.x * f2;
+      mine[1] = mine[1] * f1 + x.y * f2;
+      mine[2] = mine[2] * f1 + x.z * f2;
+      mine[3] = mine[3] * f1 + x.w * f2;
+    }
+  }
   if (!working) return;
   l += __shfl_xor(l, 32, 64);
-  if (wave_row + n >= blk.rows) return;
-  const int64_t out = (int64_t)(blk.start + token) * a.Hq + head;
+  const int mine = wave_row + opaque(n);
+  if (mine >= blk.rows) return;
+  const int64_t out = (int64_t)(blk.start + mine / group) * a.Hq + kvh * group + mine % group;
   if (blk.tiles <= plan.per) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t *dst = a.o + out * D + 4 * h;
@@ -538,8 +608,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a, Pro
     }
     if (a.lse && h == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
   } else {
-    float *base = part + ((number * a.Hkv + kvh) * plan.splits + split) * (int64_t)prompt_part_floats(D, WAVES);
-    const int r = wave * kWaveRows + n;
+    float *base = part + ((number * a.Hkv + kvh) * plan.splits + split) * (int64_t)prompt_part_floats(D);
+    const int r = mine - blk.row0;
 #pragma unroll
     for (int i = 0; i < D / 8; i++) {
       const v16f &v = o[i / 4];
@@ -558,23 +628,23 @@ template <int D>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPlan plan, const float *part) {
   constexpr int E = D / 64;
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
-  const int block_rows = plan.waves * kWaveRows, group = a.Hq / a.Hkv;
+  const int group = a.Hq / a.Hkv;
   const int64_t number = blockIdx.x / (unsigned)a.Hkv;  // few blocks are divided: one launch
   const int kvh = (int)(blockIdx.x % (unsigned)a.Hkv);
   Block blk;
-  if (!find_block(a, number, block_rows, prompt_tile_keys(D), blk) || blk.tiles <= plan.per) return;
+  if (!find_block(a, number, tile_keys(D), blk) || blk.tiles <= plan.per) return;
   const int parts = (blk.tiles + plan.per - 1) / plan.per;
-  const size_t floats = (size_t)block_rows * (D + 2);
+  constexpr size_t floats = prompt_part_floats(D);
   const float *base = part + (number * a.Hkv + kvh) * plan.splits * (int64_t)floats;
-  for (int r = blockIdx.y * 4 + wave; r < min(block_rows, blk.rows - blk.row0); r += 4 * gridDim.y) {
+  for (int r = blockIdx.y * 4 + wave; r < min(kBlockRows, blk.rows - blk.row0); r += 4 * gridDim.y) {
     float top = -INFINITY, l = 0.f, o[E] = {};
     for (int k0 = 0; k0 < parts; k0 += 8) {  // eight parts in flight
       float mp[8], lp[8], op[8][E];
 #pragma unroll
       for (int u = 0; u < 8; u++) {
         const float *p = base + (size_t)min(k0 + u, parts - 1) * floats;
-        mp[u] = p[block_rows * D + r];
-        lp[u] = p[block_rows * (D + 1) + r];
+        mp[u] = p[kBlockRows * D + r];
+        lp[u] = p[kBlockRows * (D + 1) + r];
 #pragma unroll
         for (int e = 0; e < E; e++) op[u][e] = p[r * D + E * lane + e];
       }
@@ -605,22 +675,17 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPl
   }
 }
 
-template <int D, Source SRC>
+template <int D, Source SRC, bool CAP>
 hipError_t launch(const PromptArgs &a, const PromptPlan &p, float *part, hipStream_t stream) {
   const int64_t all = (int64_t)p.blocks * a.Hkv * p.splits;
   PromptPlan q = p;
   for (int64_t first = 0; first < all; first += kPromptGrid) {
     q.first = (int)first;
-    const dim3 grid((unsigned)(all - first < kPromptGrid ? all - first : kPromptGrid)), block(64 * p.waves);
-    if (p.waves == 1)
-      hipLaunchKernelGGL((prompt_kernel<D, SRC, 1>), grid, block, 0, stream, a, q, part);
-    else if (p.waves == 2)
-      hipLaunchKernelGGL((prompt_kernel<D, SRC, 2>), grid, block, 0, stream, a, q, part);
-    else
-      hipLaunchKernelGGL((prompt_kernel<D, SRC, 4>), grid, block, 0, stream, a, q, part);
+    const dim3 grid((unsigned)(all - first < kPromptGrid ? all - first : kPromptGrid));
+    hipLaunchKernelGGL((prompt_kernel<D, SRC, CAP>), grid, dim3(64 * kBlockWaves), 0, stream, a, q, part);
   }
   if (p.splits > 1) {
-    const unsigned y = (unsigned)(p.waves * kWaveRows / 16);
+    const unsigned y = kBlockRows / 16;
     hipLaunchKernelGGL((prompt_join_kernel<D>), dim3((unsigned)p.blocks * (unsigned)a.Hkv, y), dim3(256), 0, stream, a, p,
                        (const float *)part);
   }
@@ -629,8 +694,13 @@ hipError_t launch(const PromptArgs &a, const PromptPlan &p, float *part, hipStre
 
 template <int D>
 hipError_t launch_dim(const PromptArgs &a, const PromptPlan &p, float *part, hipStream_t stream) {
-  if (!a.block_table) return launch<D, Source::kRows>(a, p, part, stream);
-  return a.k_scale ? launch<D, Source::kCodes>(a, p, part, stream) : launch<D, Source::kCache>(a, p, part, stream);
+  auto with = [&](auto source) {
+    constexpr Source kSrc = decltype(source)::value;
+    return a.softcap > 0.f ? launch<D, kSrc, true>(a, p, part, stream) : launch<D, kSrc, false>(a, p, part, stream);
+  };
+  if (!a.block_table) return with(std::integral_constant<Source, Source::kRows>{});
+  return a.k_scale ? with(std::integral_constant<Source, Source::kCodes>{})
+                   : with(std::integral_constant<Source, Source::kCache>{});
 }
 
 }  // namespace
@@ -638,7 +708,7 @@ hipError_t launch_dim(const PromptArgs &a, const PromptPlan &p, float *part, hip
 size_t prompt_partial_bytes(const PromptArgs &a, int cus) {
   const PromptPlan p = plan_prompt(a, cus);
   return p.splits == 1 ? 0
-                       : (size_t)p.blocks * a.Hkv * p.splits * prompt_part_floats(a.D, p.waves) * sizeof(float);
+                       : (size_t)p.blocks * a.Hkv * p.splits * prompt_part_floats(a.D) * sizeof(float);
 }
 
 hipError_t launch_prompt_attention(const PromptArgs &a, float *part, hipStream_t stream) {
