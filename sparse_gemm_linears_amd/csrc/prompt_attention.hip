@@ -48,7 +48,9 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) v2i lds_v2i;
 
 __device__ __forceinline__ v8bf as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(v8bf, (v4u{a, b, c, d}));
@@ -76,6 +78,12 @@ __device__ __forceinline__ void step_ends() {
 
 // A barrier for LDS alone: unlike __syncthreads it does not wait for the copies under way.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Two e4m3 codes (the low or the high half of w) as packed bf16, exactly.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+}
 
 enum class Source { kRows, kCache, kCodes };  // strided bf16 rows, a bf16 cache, an e4m3 cache
 
@@ -166,8 +174,13 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   constexpr bool kPaged = SRC != Source::kRows, kFp8 = SRC == Source::kCodes;
   constexpr int KT = tile_keys(D), WAVES = kBlockWaves, kRow = 2 * D;  // bytes of an LDS row
   __shared__ __align__(1024) uint8_t lds_k0[KT * kRow], lds_k1[KT * kRow], lds_v0[KT * kRow], lds_v1[KT * kRow];
-  __shared__ __align__(16) float lds_s0[kFp8 ? 2 * KT : 1], lds_s1[kFp8 ? 2 * KT : 1];
-  __shared__ __align__(16) uint16_t lds_odd[KT * D / 8];  // of a chunk of eight values, two bits for each
+  // waves of a block of at most 32 rows, each with tiles of 32 keys of its own
+  constexpr int kBytes = kFp8 ? 1 : 2, kLine = D * kBytes;  // of a value and a cache line in memory
+  constexpr int kFewTile = 32 * kLine, kFewWaves = KT * kRow / kFewTile < WAVES ? KT * kRow / kFewTile : WAVES;
+  __shared__ __align__(16) float lds_s0[kFp8 ? 64 * WAVES : 1], lds_s1[kFp8 ? 64 * WAVES : 1];
+  constexpr int kOddKeys = 32 * kFewWaves > KT ? 32 * kFewWaves : KT;
+  // of a chunk of eight values, two bits for each; at the end 512 bytes of up to three waves
+  __shared__ __align__(16) uint16_t lds_odd[kOddKeys * D / 8 > 768 ? kOddKeys * D / 8 : 768];
   __shared__ int lds_any[2];
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), n = lane & 31, h = lane >> 5;
   const int group = a.Hq / a.Hkv;
@@ -180,13 +193,15 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   const int tile0 = split * plan.per, tile_end = min(blk.tiles, tile0 + plan.per);
   if (split > 0 && tile0 >= blk.tiles) return;
 
-  // Blocks of more than 64 rows: a wave takes 32 of them and all keys of a tile.  Smaller ones: two
-  // waves share 32 rows and take 32 keys of a tile each, so that half the waves are not idle.
-  const bool shared = KT == 64 && min(kBlockRows, blk.rows - blk.row0) <= 2 * kWaveRows;
+  // Blocks of more than 64 rows: a wave takes 32 of them and all keys of a tile.  Of 33 to 64: two
+  // waves share 32 rows and take 32 keys of a tile each.  Smaller ones: the waves share all
+  // rows, and each goes over tiles of 32 keys of its own.
+  const int filled = min(kBlockRows, blk.rows - blk.row0);
+  const bool few = filled <= kWaveRows, shared = KT == 64 && !few && filled <= 2 * kWaveRows;
   const int half = shared ? wave & 1 : 0;  // of the tile's keys
   // the wave's rows; rows past the last one repeat it and are not stored
-  const int wave_row = blk.row0 + (shared ? wave >> 1 : wave) * kWaveRows;
-  const bool working = wave_row < blk.rows;
+  const int wave_row = blk.row0 + (few ? 0 : shared ? wave >> 1 : wave) * kWaveRows;
+  const bool working = few ? wave < kFewWaves : wave_row < blk.rows;
   const int row = min(wave_row + n, blk.rows - 1), token = row / group;
   auto low_of = [&](int place) { return a.window > 0 ? place - a.window + 1 : 0; };
   const int place = blk.place0 + token;
@@ -205,12 +220,13 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 
   v8bf qf[D / 16];
   {
-    const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head + 8 * h;
+    const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head;
+    const int first = kFp8 && few ? 16 * h : 8 * h, odd_step = kFp8 && few ? 8 : 16;  // few_key_frags' order, or key_frag's
     // the weights' exponents grow with the scores: a negative scale turns the queries over
     const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int s = 0; s < D / 16; s++) {
-      const uint4 raw = *reinterpret_cast<const uint4 *>(src + 16 * s);
+      const uint4 raw = *reinterpret_cast<const uint4 *>(src + first + 32 * (s >> 1) + odd_step * (s & 1));
       qf[s] = as_bf16x8(raw.x ^ sign, raw.y ^ sign, raw.z ^ sign, raw.w ^ sign);
     }
   }
@@ -240,7 +256,6 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   auto run_line = [&](int key0, int run) FP8LIN_INLINE -> int64_t {
     return kPaged ? from_lane(found, (key0 - found_from) / 16 + run) : (int64_t)blk.start + key0 + 16 * run;
   };
-  constexpr int kBytes = kFp8 ? 1 : 2;  // of a value in memory
   const int64_t k_line = kPaged ? D * kBytes : a.k_token * 2, v_line = kPaged ? D * kBytes : a.v_token * 2;
   const char *k_base = static_cast<const char *>(a.k) + (kPaged ? 0 : (int64_t)kvh * a.k_head * 2);
   const char *v_base = static_cast<const char *>(a.v) + (kPaged ? 0 : (int64_t)kvh * a.v_head * 2);
@@ -315,8 +330,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       uint32_t b[8];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        b[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.0f, false));
-        b[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.0f, true));
+        b[2 * j] = e4m3x2_to_bf16<false>(w[j]);
+        b[2 * j + 1] = e4m3x2_to_bf16<true>(w[j]);
       }
       *reinterpret_cast<uint4 *>(row_at + 16 * c0) = make_uint4(b[0], b[1], b[2], b[3]);
       *reinterpret_cast<uint4 *>(row_at + 16 * c1) = make_uint4(b[4], b[5], b[6], b[7]);
@@ -351,35 +366,35 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     return __builtin_bit_cast(v8bf, (v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}));
   };
 
-  // edge: some row of the wave does not see some key of the tile; odd: lds_odd has values
-  // that were taken out of the tile.
-  auto use_tile = [&](auto subs, int key0, uint8_t *lk, uint8_t *lv, const float *ls, bool edge, bool odd) FP8LIN_INLINE {
-    constexpr int S = decltype(subs)::value;
-    // Fragments are read a few steps ahead of the products that take them, and no earlier: the
-    // compiler would fill the registers with them.
-    constexpr int kKeyRing = S == 2 ? 3 : 4, kSteps = D / 16;
-    const int ka = opaque(key_at);
-    v16f sc[S];
-    v8bf kf[kKeyRing][S];
-    auto read_keys = [&](int s) FP8LIN_INLINE {
+  // The rows that see a value that was taken out of a tile get what a sum with it is.  (keys: of
+  // the tile at key0; at: of the first one in lds_odd)
+  auto put_odd = [&](int key0, int keys, int at) FP8LIN_INLINE {
+    uint32_t flags[D / 16] = {};  // of the values of the keys that the row sees
+#pragma unroll 1
+    for (int key = max(0, seen_low - key0); key < min(keys, seen_end - key0); key++) {
+      const uint4 *from = reinterpret_cast<const uint4 *>(lds_odd + (key + at) * (D / 8));
 #pragma unroll
-      for (int sub = 0; sub < S; sub++) kf[s % kKeyRing][sub] = key_frag(lk, ka, sub, s);
-    };
-#pragma unroll
-    for (int s = 0; s + 1 < kKeyRing; s++) read_keys(s);
-#pragma unroll
-    for (int sub = 0; sub < S; sub++)
-#pragma unroll
-      for (int j = 0; j < 16; j++) sc[sub][j] = 0.f;
-#pragma unroll
-    for (int s = 0; s < kSteps; s++) {
-      if (s + kKeyRing - 1 < kSteps) read_keys(s + kKeyRing - 1);
-      step_ends();
-#pragma unroll
-      for (int sub = 0; sub < S; sub++)
-        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % kKeyRing][sub], qf[s], sc[sub], 0, 0, 0);
-      step_ends();
+      for (int w = 0; w < D / 64; w++) {
+        const uint4 f = from[w];
+        flags[4 * w] |= f.x;
+        flags[4 * w + 1] |= f.y;
+        flags[4 * w + 2] |= f.z;
+        flags[4 * w + 3] |= f.w;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < D / 8; i++) {
+      const uint32_t f = flags[i / 2] >> (16 * (i & 1) + 8 * h);
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        o[i / 4][4 * (i % 4) + j] += (f >> 2 * j & 1 ? INFINITY : 0.f) - (f >> 2 * j & 2 ? INFINITY : 0.f);
+    }
+  };
+  // Weights of the scores sc of 32 S keys from key0 on.  before: what is done between the
+  // maximum and the exponentials.  edge: some row of the wave does not see some of the keys.
+  auto weigh = [&](auto subs, const v16f(&sc)[decltype(subs)::value], v8bf(&p)[2 * decltype(subs)::value], int key0,
+                   const float *ks, const float *vs, bool edge, auto before) FP8LIN_INLINE {
+    constexpr int S = decltype(subs)::value;
     float x[16 * S];
 #pragma unroll
     for (int j = 0; j < 16 * S; j++) x[j] = sc[j / 16][j % 16];
@@ -387,11 +402,11 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 #pragma unroll
       for (int j = 0; j < 4 * S; j++) {
         if (j % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-        const float4 ks = *reinterpret_cast<const float4 *>(ls + 8 * j + 4 * h);
-        x[4 * j] *= ks.x;
-        x[4 * j + 1] *= ks.y;
-        x[4 * j + 2] *= ks.z;
-        x[4 * j + 3] *= ks.w;
+        const float4 g = *reinterpret_cast<const float4 *>(ks + 8 * j + 4 * h);
+        x[4 * j] *= g.x;
+        x[4 * j + 1] *= g.y;
+        x[4 * j + 2] *= g.z;
+        x[4 * j + 3] *= g.w;
       }
     }
     if constexpr (CAP) {
@@ -421,13 +436,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 #pragma unroll
       for (int i = 0; i < D / 32; i++) o[i] *= shrink;
     }
-    constexpr int kDb = D / 32, kProducts = kDb * 2 * S, kValueRing = 4;
-    const int va = opaque(value_at);
-    v8bf vf[kValueRing];
-    auto read_values = [&](int i) FP8LIN_INLINE { vf[i % kValueRing] = value_frag(lv, va, i % kDb, i / kDb); };
-#pragma unroll
-    for (int i = 0; i + 1 < kValueRing; i++) read_values(i);
-    step_ends();
+    before();
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < 16 * S; j++) x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], rate, -base));
@@ -441,22 +450,63 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 #pragma unroll
       for (int j = 0; j < 4 * S; j++) {
         if (j % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-        const float4 vs = *reinterpret_cast<const float4 *>(ls + KT + 8 * j + 4 * h);
-        x[4 * j] *= vs.x;
-        x[4 * j + 1] *= vs.y;
-        x[4 * j + 2] *= vs.z;
-        x[4 * j + 3] *= vs.w;
+        const float4 g = *reinterpret_cast<const float4 *>(vs + 8 * j + 4 * h);
+        x[4 * j] *= g.x;
+        x[4 * j + 1] *= g.y;
+        x[4 * j + 2] *= g.z;
+        x[4 * j + 3] *= g.w;
       }
       if (edge) {  // a scale that is not finite belongs to no row that does not see its key
 #pragma unroll
         for (int j = 0; j < 16 * S; j++) x[j] = live(j) ? x[j] : 0.f;
       }
     }
-    v8bf p[2 * S];
 #pragma unroll
     for (int s = 0; s < 2 * S; s++)
       p[s] = as_bf16x8(pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
                        pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7]));
+  };
+
+  // One tile; odd: lds_odd has values
+  // that were taken out of the tile.
+  auto use_tile = [&](auto subs, int key0, uint8_t *lk, uint8_t *lv, const float *ks, const float *vs,
+                      bool edge, bool odd) FP8LIN_INLINE {
+    constexpr int S = decltype(subs)::value;
+    // Fragments are read a few steps ahead of the products that take them, and no earlier: the
+    // compiler would fill the registers with them.
+    constexpr int kKeyRing = S == 2 ? 3 : 4, kSteps = D / 16;
+    const int ka = opaque(key_at);
+    v16f sc[S];
+    v8bf kf[kKeyRing][S];
+    auto read_keys = [&](int s) FP8LIN_INLINE {
+#pragma unroll
+      for (int sub = 0; sub < S; sub++) kf[s % kKeyRing][sub] = key_frag(lk, ka, sub, s);
+    };
+#pragma unroll
+    for (int s = 0; s + 1 < kKeyRing; s++) read_keys(s);
+#pragma unroll
+    for (int sub = 0; sub < S; sub++)
+#pragma unroll
+      for (int j = 0; j < 16; j++) sc[sub][j] = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; s++) {
+      if (s + kKeyRing - 1 < kSteps) read_keys(s + kKeyRing - 1);
+      step_ends();
+#pragma unroll
+      for (int sub = 0; sub < S; sub++)
+        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % kKeyRing][sub], qf[s], sc[sub], 0, 0, 0);
+      step_ends();
+    }
+    constexpr int kDb = D / 32, kProducts = kDb * 2 * S, kValueRing = 4;
+    const int va = opaque(value_at);
+    v8bf vf[kValueRing];
+    auto read_values = [&](int i) FP8LIN_INLINE { vf[i % kValueRing] = value_frag(lv, va, i % kDb, i / kDb); };
+    v8bf p[2 * S];
+    weigh(subs, sc, p, key0, ks, vs, edge, [&]() FP8LIN_INLINE {
+#pragma unroll
+      for (int i = 0; i + 1 < kValueRing; i++) read_values(i);
+      step_ends();
+    });
 #pragma unroll
     for (int i = 0; i < kProducts; i++) {
       if (i + kValueRing - 1 < kProducts) read_values(i + kValueRing - 1);
@@ -464,29 +514,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       o[i % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i % kValueRing], p[i / kDb], o[i % kDb], 0, 0, 0);
       step_ends();
     }
-    if (__builtin_expect(odd, 0)) {
-      // The rows that see such a value get what a sum with it is.
-      uint32_t flags[D / 16] = {};  // of the values of the keys that the row sees
-#pragma unroll 1
-      for (int key = max(0, seen_low - key0); key < min(32 * S, seen_end - key0); key++) {
-        const uint4 *at = reinterpret_cast<const uint4 *>(lds_odd + (key + 32 * half) * (D / 8));
-#pragma unroll
-        for (int w = 0; w < D / 64; w++) {
-          const uint4 f = at[w];
-          flags[4 * w] |= f.x;
-          flags[4 * w + 1] |= f.y;
-          flags[4 * w + 2] |= f.z;
-          flags[4 * w + 3] |= f.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < D / 8; i++) {
-        const uint32_t f = flags[i / 2] >> (16 * (i & 1) + 8 * h);
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          o[i / 4][4 * (i % 4) + j] += (f >> 2 * j & 1 ? INFINITY : 0.f) - (f >> 2 * j & 2 ? INFINITY : 0.f);
-      }
-    }
+    if (__builtin_expect(odd, 0)) put_odd(key0, 32 * S, 32 * half);
   };
   // 0 times an infinity or a NaN is a NaN, and such a value must not reach rows that do not see
   // its key: they are taken out of a tile of values and noted in lds_odd.
@@ -543,7 +571,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       bool odd = false;
       if (key0 + KT > block_end || key0 < block_low) odd = take_odd(lv, kOdd);
       if (working && mine < any_end && mine + kMine > any_low)
-        use_tile(subs, mine, lk, lv, ls + 32 * half, mine + kMine > all_end || mine < all_low, odd);
+        use_tile(subs, mine, lk, lv, ls + 32 * half, ls + KT + 32 * half, mine + kMine > all_end || mine < all_low, odd);
     };
     if (tile0 < tile_end) fetch(tile0, lds_k0, lds_v0);
     for (int t = tile0; t < tile_end; t += 2) {
@@ -551,7 +579,174 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       if (t + 1 < tile_end) step(t + 1, std::true_type{});
     }
   };
-  if constexpr (KT == 64) {
+  // Blocks of at most 32 rows.  A wave's tile of 32 keys lies in LDS as it lies in memory (codes
+  // become bf16 when they are read: no other wave reads them); the copies of the next
+  // tile are under way while one is used, and no wave waits for another.
+  auto raw_swizzle = [&](int r, int c) FP8LIN_INLINE { return c ^ (D == 64 ? r >> 2 & 3 : D == 128 ? r >> 1 & 7 : r & 15); };
+  auto few_tiles = [&]() FP8LIN_INLINE {
+    constexpr int kFewCopies = 32 / kCopyRows, kLoads = 2 * kFewCopies + (kFp8 ? 1 : 0);
+    const int key_begin = blk.begin + tile0 * KT, key_end = min(blk.end, blk.begin + tile_end * KT);
+    const int tiles = (key_end - key_begin + 31) / 32;
+    auto key_of = [&](int i) FP8LIN_INLINE { return key_begin + 32 * (wave + kFewWaves * i); };  // of the wave's tile i
+    const int rl = lane / kLanes, cl = lane % kLanes;
+    auto place = [&](auto keys, int r, int c) FP8LIN_INLINE {  // source chunk of position c of row r
+      constexpr bool kKeys = decltype(keys)::value;
+      return kFp8 ? raw_swizzle(r, c) : kKeys ? key_swizzle<D>(r, c) : value_swizzle<D>(r, c);
+    };
+    int64_t runs = 0;  // of a cache: lane x holds the line of run x % 2 of the wave's tile 32 j + x / 2
+    auto fetch = [&](int i, uint8_t *lk, uint8_t *lv, float *ls) FP8LIN_INLINE {
+      const int key0 = key_of(i);
+      if constexpr (kPaged) {
+        if (i % 32 == 0) {
+          const int key = key_of(i + (lane >> 1)) + 16 * (lane & 1);
+          if (key < blk.end) {
+            const int p = (int)((uint32_t)key / (uint32_t)a.page_size);
+            const int page = min(max(a.block_table[(int64_t)blk.b * a.max_pages + p], 0), a.pages - 1);
+            runs = ((int64_t)page * a.Hkv + kvh) * a.page_size + (key - p * a.page_size);
+          }
+        }
+      }
+      const bool full = key0 >= blk.lowest && key0 + 32 <= blk.end;
+      auto line_of = [&](int run) FP8LIN_INLINE -> int64_t {
+        return kPaged ? from_lane(runs, 2 * (i % 32) + run) : (int64_t)blk.start + key0 + 16 * run;
+      };
+      auto copy = [&](auto keys, int j, const char *base, int64_t line, uint8_t *to) FP8LIN_INLINE {
+        const int r0 = j * kCopyRows;  // and rl: a copy's rows differ from the first one's by whole bits
+        const int flip = place(keys, r0, 0);
+        int run = r0 >> 4;
+        uint32_t at;
+        if (full) {
+          at = (uint32_t)(((r0 & 15) + rl) * (int)line + 16 * (place(keys, rl, cl) ^ flip));
+        } else {
+          const int src = near(key0, r0 + opaque(rl));
+          run = uniform(near(key0, r0)) >> 4;
+          at = (uint32_t)((src & 15) * (int)line + 16 * (place(keys, rl, cl) ^ flip));
+        }
+        copy16_global_to_lds(base + line_of(run) * line + at, to + wave * kFewTile + r0 * kLine);
+      };
+#pragma unroll
+      for (int j = 0; j < kFewCopies; j++) copy(std::true_type{}, j, k_base, k_line, lk);
+#pragma unroll
+      for (int j = 0; j < kFewCopies; j++) copy(std::false_type{}, j, v_base, v_line, lv);
+      if constexpr (kFp8) {  // lanes 0 .. 31 the keys' scales, the others the values'
+        const int src = near(key0, n);
+        const int64_t at = (src >> 4 ? line_of(1) : line_of(0)) + (src & 15);
+        __builtin_amdgcn_global_load_lds((glb_void *)const_cast<float *>((h ? a.v_scale : a.k_scale) + at),
+                                         (lds_void *)(ls + 64 * wave), 4, 0, 0);
+      }
+      step_ends();
+    };
+    const int few_key = kFp8 ? wave * kFewTile + n * kLine + 16 * raw_swizzle(n, h)
+                             : wave * kFewTile + n * kLine + 16 * key_swizzle<D>(n, h);
+    const int vr = kFp8 ? 4 * h + (lane >> 1 & 3) + 8 * (lane >> 3 & 1) : value_r, dh = lane >> 4 & 1;
+    const int few_value = wave * kFewTile + vr * kLine + 8 * (lane & 1) +
+                          16 * (kFp8 ? raw_swizzle(vr, dh) : value_swizzle<D>(vr, 2 * dh + (lane & 3) / 2));
+    auto bf16_of = [&](uint32_t w0, uint32_t w1) FP8LIN_INLINE {
+      return as_bf16x8(e4m3x2_to_bf16<false>(w0), e4m3x2_to_bf16<true>(w0), e4m3x2_to_bf16<false>(w1),
+                       e4m3x2_to_bf16<true>(w1));
+    };
+    auto few_value_frag = [&](uint8_t *lv, int at, int db, int step) FP8LIN_INLINE {
+      if constexpr (!kFp8) {
+        return value_frag(lv, at, db, step);
+      } else {
+        const v2i raw = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(lv + (at ^ 32 * db) + 16 * step * kLine));
+        return bf16_of((uint32_t)raw[0], (uint32_t)raw[1]);
+      }
+    };
+    // Values that are not finite, as in take_odd, in the wave's own tile.
+    auto take_few_odd = [&](uint8_t *lv, float *vs) FP8LIN_INLINE -> bool {
+      constexpr int kParts = kFewTile / 16;
+      const int self = opaque(lane);
+      uint8_t *const mine = lv + wave * kFewTile;
+      auto finite = [](float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; };
+      bool found_one = false;
+      if (kFp8 && self < 32) found_one = !finite(vs[self]);
+      for (int i = self; i < kParts; i += 64) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(mine + 16 * i);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          found_one |= (kFp8 ? ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : not_finite(w[j])) != 0;
+      }
+      if (__builtin_expect(!__any(found_one), 1)) return false;
+#pragma unroll 1
+      for (int i = self; i < kParts; i += 64) {
+        constexpr int kChunks = kLine / 16, kEach = 16 / kBytes;
+        uint32_t *at = reinterpret_cast<uint32_t *>(mine + 16 * i);
+        const int r = i / kChunks, c = place(std::false_type{}, r, i % kChunks);
+        uint32_t flags = 0;
+#pragma unroll 1
+        for (int j = 0; j < kEach; j++) {
+          const int word = j * kBytes / 4, shift = 8 * (j * kBytes % 4);
+          const uint32_t bits = at[word] >> shift & (kFp8 ? 0xFFu : 0xFFFFu);
+          float v = bf16_to_f32(bits);
+          if constexpr (kFp8) v = bf16_to_f32(e4m3x2_to_bf16<false>(bits) & 0xFFFFu) * vs[r];
+          if (finite(v)) continue;
+          at[word] &= ~((kFp8 ? 0xFFu : 0xFFFFu) << shift);
+          flags |= (v != v ? 3u : v < 0.f ? 2u : 1u) << 2 * j;
+        }
+        uint16_t *to = lds_odd + (32 * wave + r) * (D / 8) + c * kEach / 8;
+        to[0] = (uint16_t)flags;
+        if constexpr (kFp8) to[1] = (uint16_t)(flags >> 16);
+      }
+      step_ends();
+      if (kFp8 && self < 32 && !finite(vs[self])) vs[self] = 0.f;
+      step_ends();
+      return true;
+    };
+    auto step = [&](int i, auto stage) FP8LIN_INLINE {
+      constexpr bool kOdd = decltype(stage)::value;
+      uint8_t *lk = kOdd ? lds_k1 : lds_k0, *lv = kOdd ? lds_v1 : lds_v0;
+      float *ls = (kOdd ? lds_s1 : lds_s0) + 64 * wave * (kFp8 ? 1 : 0);
+      if (wave + kFewWaves * (i + 1) < tiles) {
+        fetch(i + 1, kOdd ? lds_k0 : lds_k1, kOdd ? lds_v0 : lds_v1, kOdd ? lds_s0 : lds_s1);
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (kLoads & 15) | (kLoads >> 4) << 14);  // all but the copies just begun
+      } else {
+        wait_global_loads();
+      }
+      step_ends();
+      const int key0 = key_of(i);
+      const bool edge = key0 + 32 > all_end || key0 < all_low;
+      const bool odd = edge && take_few_odd(lv, ls + 32);
+      v16f sc[1];
+#pragma unroll
+      for (int j = 0; j < 16; j++) sc[0][j] = 0.f;
+      const int ka = opaque(few_key), va = opaque(few_value);
+      if constexpr (kFp8) {
+#pragma unroll
+        for (int c = 0; c < D / 32; c++) {
+          const uint4 raw = *reinterpret_cast<const uint4 *>(lk + (ka ^ 32 * c));
+          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of(raw.x, raw.y), qf[2 * c], sc[0], 0, 0, 0);
+          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of(raw.z, raw.w), qf[2 * c + 1], sc[0], 0, 0, 0);
+          if (c % 4 == 3) step_ends();
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < D / 16; s++) {
+          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(lk, ka, 0, s), qf[s], sc[0], 0, 0, 0);
+          if (s % 4 == 3) step_ends();
+        }
+      }
+      v8bf p[2];
+      weigh(std::integral_constant<int, 1>{}, sc, p, key0, ls, ls + 32, edge, [] {});
+#pragma unroll
+      for (int j = 0; j < 2 * (D / 32); j++) {
+        const int db = j % (D / 32), s = j / (D / 32);
+        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(few_value_frag(lv, va, db, s), p[s], o[db], 0, 0, 0);
+        if (j % 4 == 3) step_ends();
+      }
+      if (__builtin_expect(odd, 0)) put_odd(key0, 32, 32 * wave);
+    };
+    if (wave >= tiles) return;
+    fetch(0, lds_k0, lds_v0, lds_s0);
+    for (int i = 0; wave + kFewWaves * i < tiles; i += 2) {
+      step(i, std::false_type{});
+      if (wave + kFewWaves * (i + 1) < tiles) step(i + 1, std::true_type{});
+    }
+  };
+  if (few) {
+    if (working) few_tiles();
+  } else if constexpr (KT == 64) {
     if (shared)
       all_tiles(std::integral_constant<int, 1>{});
     else
@@ -560,35 +755,45 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     all_tiles(std::integral_constant<int, 1>{});
   }
 
-  if (shared) {
-    // the second wave of a pair hands its state to the first, lane by lane
+  if (few || shared) {
+    // The other waves of the rows hand their states to the first, lane by lane: each has a box
+    // for o, and 512 bytes for m and l.
+    auto box = [&](int slot, int i) FP8LIN_INLINE {
+      const int part = D == 256 ? 2 * slot + i / 16 : slot, at = D == 256 ? i % 16 : i;
+      uint8_t *base = part == 0 ? lds_k0 : part == 1 ? lds_k1 : part == 2 ? lds_v0 : lds_v1;
+      return reinterpret_cast<float4 *>(base) + 64 * at + lane;
+    };
+    float *ml = reinterpret_cast<float *>(lds_odd);
+    const int slot = few ? wave - 1 : wave >> 1;
+    const bool gives = working && (few ? wave > 0 : half == 1);
     __syncthreads();
-    float *box = reinterpret_cast<float *>(wave < 2 ? lds_k0 : lds_k1);
-    float *box_ml = reinterpret_cast<float *>(wave < 2 ? lds_v0 : lds_v1);
-    if (half == 1 && working) {
+    if (gives) {
 #pragma unroll
       for (int i = 0; i < D / 8; i++)
-        *reinterpret_cast<float4 *>(box + 256 * i + 4 * lane) =
-            make_float4(o[i / 4][4 * (i % 4)], o[i / 4][4 * (i % 4) + 1], o[i / 4][4 * (i % 4) + 2],
-                        o[i / 4][4 * (i % 4) + 3]);
-      box_ml[lane] = m;
-      box_ml[64 + lane] = l;
+        *box(slot, i) = make_float4(o[i / 4][4 * (i % 4)], o[i / 4][4 * (i % 4) + 1], o[i / 4][4 * (i % 4) + 2],
+                                    o[i / 4][4 * (i % 4) + 3]);
+      ml[128 * slot + lane] = m;
+      ml[128 * slot + 64 + lane] = l;
     }
     __syncthreads();
-    if (half == 1) return;
-    const float m2 = box_ml[lane], top = fmaxf(m, m2);
-    const float f1 = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
-    const float f2 = m2 == top ? 1.f : __builtin_amdgcn_exp2f(m2 - top);
-    m = top;
-    l = l * f1 + box_ml[64 + lane] * f2;
+    if (gives || (few && wave > 0)) return;
+    const int end = few ? kFewWaves - 1 : slot + 1;
+    if (!working) return;
+    for (int from = few ? 0 : slot; from < end; from++) {
+      const float m2 = ml[128 * from + lane], top = fmaxf(m, m2);
+      const float f1 = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
+      const float f2 = m2 == top ? 1.f : __builtin_amdgcn_exp2f(m2 - top);
+      m = top;
+      l = l * f1 + ml[128 * from + 64 + lane] * f2;
 #pragma unroll
-    for (int i = 0; i < D / 8; i++) {
-      const float4 x = *reinterpret_cast<const float4 *>(box + 256 * i + 4 * lane);
-      float *mine = reinterpret_cast<float *>(&o[i / 4]) + 4 * (i % 4);
-      mine[0] = mine[0] * f1 + x.x * f2;
-      mine[1] = mine[1] * f1 + x.y * f2;
-      mine[2] = mine[2] * f1 + x.z * f2;
-      mine[3] = mine[3] * f1 + x.w * f2;
+      for (int i = 0; i < D / 8; i++) {
+        const float4 x = *box(from, i);
+        float *mine = reinterpret_cast<float *>(&o[i / 4]) + 4 * (i % 4);
+        mine[0] = mine[0] * f1 + x.x * f2;
+        mine[1] = mine[1] * f1 + x.y * f2;
+        mine[2] = mine[2] * f1 + x.z * f2;
+        mine[3] = mine[3] * f1 + x.w * f2;
+      }
     }
   }
   if (!working) return;
