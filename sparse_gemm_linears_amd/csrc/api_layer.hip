@@ -152,6 +152,7 @@ fp8l_status prompt(PromptArgs a, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, 
   a.window = (int)(window < kMaxTokens ? window : kMaxTokens);
   // a smaller cap has no reciprocal, and leaves scores that no exponential tells from 0 either
   if (a.softcap > 0.0f && a.softcap < 1e-30f) a.softcap = 1e-30f;
+  if (a.softcap > 1e38f) a.softcap = 1e38f;  // log2(e) times it is finite; scores are as good as without one either way
   // scores of a scale of 0 are 0 under any cap; without one 0 times the -infinity of a hidden key would be a NaN
   if (a.scale == 0.0f && a.softcap == 0.0f) a.softcap = 1.0f;
   CallScratch sc;

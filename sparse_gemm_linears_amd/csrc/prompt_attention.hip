@@ -145,27 +145,33 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-// c tanh(x / c) of each value.  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that would
-// lose a small score's low bits, its power series (2^-26 of it is left out).
+// tanh of each value.  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that would lose a
+// small score's low bits, its power series (2^-26 of it is left out).
 template <int N>
-__device__ __forceinline__ void cap_scores(float (&x)[N], float cap) {
-  const float rate = 1.f / cap;
+__device__ __forceinline__ void tanh_each(float (&z)[N]) {
   float most = 0.f;
 #pragma unroll
-  for (int j = 0; j < N; j++) most = fmaxf(most, fabsf(x[j] * rate));
-  const bool large = __any(!(most < 0.25f));
+  for (int j = 0; j < N; j++) most = fmaxf(most, fabsf(z[j]));
+  // (a NaN stays one on either way)
+  if (__any(most >= 0.25f)) {
 #pragma unroll
-  for (int j = 0; j < N; j++) {
-    const float z = x[j] * rate, u = z * z;
-    float t = __builtin_fmaf(u, 62.f / 2835.f, -17.f / 315.f);
-    t = __builtin_fmaf(u, t, 2.f / 15.f);
-    t = __builtin_fmaf(u, t, -1.f / 3.f);
-    float y = cap * __builtin_fmaf(z * u, t, z);
-    if (large) {
-      const float m = fabsf(z), e = __builtin_amdgcn_exp2f(2.f * kLog2e * m);
-      if (!(m < 0.25f)) y = cap * copysignf(1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e), z);
+    for (int j = 0; j < N; j++) {
+      const float w = fabsf(z[j]), u = z[j] * z[j], e = __builtin_amdgcn_exp2f(2.f * kLog2e * w);
+      float t = __builtin_fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+      t = __builtin_fmaf(u, t, 2.f / 15.f);
+      t = __builtin_fmaf(u, t, -1.f / 3.f);
+      t = __builtin_fmaf(z[j] * u, t, z[j]);
+      z[j] = w >= 0.25f ? copysignf(1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e), z[j]) : t;
     }
-    x[j] = y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const float u = z[j] * z[j];
+      float t = __builtin_fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+      t = __builtin_fmaf(u, t, 2.f / 15.f);
+      t = __builtin_fmaf(u, t, -1.f / 3.f);
+      z[j] = __builtin_fmaf(z[j] * u, t, z[j]);
+    }
   }
 }
 
@@ -182,6 +188,10 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   // of a chunk of eight values, two bits for each; at the end 512 bytes of up to three waves
   __shared__ __align__(16) uint16_t lds_odd[kOddKeys * D / 8 > 768 ? kOddKeys * D / 8 : 768];
   __shared__ int lds_any[2];
+  // Of 256-wide heads the last query fragments stay in LDS: the registers would not hold them, and a
+  // reload from scratch memory waits for the copies under way.
+  constexpr int kHeld = D == 256 ? D / 16 - (kFp8 ? 2 : 3) : D / 16;  // fragments in registers
+  __shared__ __align__(16) uint4 lds_q[kHeld < D / 16 ? (D / 16 - kHeld) * 64 * WAVES : 1];
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), n = lane & 31, h = lane >> 5;
   const int group = a.Hq / a.Hkv;
   const uint32_t self = (uint32_t)plan.first + blockIdx.x, rest = self / (uint32_t)a.Hkv;
@@ -218,7 +228,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   const int block_low = low_of(blk.place0 + (min(blk.row0 + kBlockRows, blk.rows) - 1) / group);
   if (threadIdx.x < 2) lds_any[threadIdx.x] = 0;  // (before the first barrier)
 
-  v8bf qf[D / 16];
+  v8bf qf[kHeld];
   {
     const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head;
     const int first = kFp8 && few ? 16 * h : 8 * h, odd_step = kFp8 && few ? 8 : 16;  // few_key_frags' order, or key_frag's
@@ -227,16 +237,23 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 #pragma unroll
     for (int s = 0; s < D / 16; s++) {
       const uint4 raw = *reinterpret_cast<const uint4 *>(src + first + 32 * (s >> 1) + odd_step * (s & 1));
-      qf[s] = as_bf16x8(raw.x ^ sign, raw.y ^ sign, raw.z ^ sign, raw.w ^ sign);
+      const v8bf f = as_bf16x8(raw.x ^ sign, raw.y ^ sign, raw.z ^ sign, raw.w ^ sign);
+      if (s < kHeld)
+        qf[s] = f;
+      else
+        lds_q[((s - kHeld) * WAVES + wave) * 64 + lane] = __builtin_bit_cast(uint4, f);
     }
   }
+  auto query = [&](int s) FP8LIN_INLINE {
+    return s < kHeld ? qf[s] : __builtin_bit_cast(v8bf, lds_q[((s - kHeld) * WAVES + wave) * 64 + lane]);
+  };
   v16f o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; i++)
 #pragma unroll
     for (int j = 0; j < 16; j++) o[i][j] = 0.f;
   float m = -INFINITY, l = 0.f;
-  const float scale = fabsf(a.scale);
+  const float scale = fabsf(a.scale), to_tanh = CAP ? scale / a.softcap : 0.f;
 
   // Copies.  Keys are taken in runs of 16 (which lie in one page): a wave's copy of 64 x 16
   // bytes covers a few rows of one run, at an address that the wave shares and offsets of
@@ -303,7 +320,12 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 #pragma unroll
       for (int i = 0; i < kCopiesPer; i++) {
         if (kCopies % WAVES != 0 && copy_row(i) >= KT) break;
-        copy_rows(i, run_line(key0, copy_row(i) >> 4), k_off[i % kKinds], v_off[i % kKinds], lk, lv);
+        uint32_t ko = k_off[i % kKinds], vo = v_off[i % kKinds];
+        if constexpr (D == 256) {  // no registers to keep them
+          const int self = opaque(lane), r = copy_row(i) + self / kLanes;
+          offsets(r, self % kLanes, r, ko, vo);
+        }
+        copy_rows(i, run_line(key0, copy_row(i) >> 4), ko, vo, lk, lv);
       }
     } else {
 #pragma unroll
@@ -411,10 +433,10 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     }
     if constexpr (CAP) {
 #pragma unroll
-      for (int j = 0; j < 16 * S; j++) x[j] *= scale;
-      cap_scores(x, a.softcap);
+      for (int j = 0; j < 16 * S; j++) x[j] *= to_tanh;
+      tanh_each(x);
     }
-    const float rate = CAP ? kLog2e : scale * kLog2e;  // of the exponents in units of x
+    const float rate = (CAP ? a.softcap : scale) * kLog2e;  // of the exponents in units of x
     const int live_end = seen_end - key0 - 4 * h, live_low = seen_low - key0 - 4 * h;
     auto live = [&](int j) { return 8 * (j >> 2) + (j & 3) < live_end && 8 * (j >> 2) + (j & 3) >= live_low; };
     if (edge) {
@@ -474,7 +496,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     constexpr int S = decltype(subs)::value;
     // Fragments are read a few steps ahead of the products that take them, and no earlier: the
     // compiler would fill the registers with them.
-    constexpr int kKeyRing = S == 2 ? 3 : 4, kSteps = D / 16;
+    constexpr int kKeyRing = S == 2 ? 3 : D == 256 ? 2 : 4, kSteps = D / 16;
     const int ka = opaque(key_at);
     v16f sc[S];
     v8bf kf[kKeyRing][S];
@@ -494,10 +516,10 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       step_ends();
 #pragma unroll
       for (int sub = 0; sub < S; sub++)
-        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % kKeyRing][sub], qf[s], sc[sub], 0, 0, 0);
+        sc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % kKeyRing][sub], query(s), sc[sub], 0, 0, 0);
       step_ends();
     }
-    constexpr int kDb = D / 32, kProducts = kDb * 2 * S, kValueRing = 4;
+    constexpr int kDb = D / 32, kProducts = kDb * 2 * S, kValueRing = D == 256 ? 2 : 4;
     const int va = opaque(value_at);
     v8bf vf[kValueRing];
     auto read_values = [&](int i) FP8LIN_INLINE { vf[i % kValueRing] = value_frag(lv, va, i % kDb, i / kDb); };
@@ -716,14 +738,14 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 #pragma unroll
         for (int c = 0; c < D / 32; c++) {
           const uint4 raw = *reinterpret_cast<const uint4 *>(lk + (ka ^ 32 * c));
-          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of(raw.x, raw.y), qf[2 * c], sc[0], 0, 0, 0);
-          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of(raw.z, raw.w), qf[2 * c + 1], sc[0], 0, 0, 0);
+          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of(raw.x, raw.y), query(2 * c), sc[0], 0, 0, 0);
+          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of(raw.z, raw.w), query(2 * c + 1), sc[0], 0, 0, 0);
           if (c % 4 == 3) step_ends();
         }
       } else {
 #pragma unroll
         for (int s = 0; s < D / 16; s++) {
-          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(lk, ka, 0, s), qf[s], sc[0], 0, 0, 0);
+          sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(lk, ka, 0, s), query(s), sc[0], 0, 0, 0);
           if (s % 4 == 3) step_ends();
         }
       }
