@@ -207,7 +207,9 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   // waves share 32 rows and take 32 keys of a tile each.  Smaller ones: the waves share all
   // rows, and each goes over tiles of 32 keys of its own.
   const int filled = min(kBlockRows, blk.rows - blk.row0);
-  const bool few = filled <= kWaveRows, shared = KT == 64 && !few && filled <= 2 * kWaveRows;
+  // (not the last rows of more: their keys would wait for fewer waves)
+  const bool few = kPaged && kFewWaves > 1 && blk.rows <= kWaveRows;
+  const bool shared = KT == 64 && !few && filled <= 2 * kWaveRows;
   const int half = shared ? wave & 1 : 0;  // of the tile's keys
   // the wave's rows; rows past the last one repeat it and are not stored
   const int wave_row = blk.row0 + (few ? 0 : shared ? wave >> 1 : wave) * kWaveRows;
@@ -767,7 +769,9 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     }
   };
   if (few) {
-    if (working) few_tiles();
+    if constexpr (kPaged && kFewWaves > 1) {
+      if (working) few_tiles();
+    }
   } else if constexpr (KT == 64) {
     if (shared)
       all_tiles(std::integral_constant<int, 1>{});

@@ -48,7 +48,7 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   const int64_t resident = (int64_t)cus * 2, found = (int64_t)p.blocks * a.Hkv;
   const int64_t filled = rows / p.blocks;  // rows of a block
   const int64_t parts = resident * (filled <= 32 ? 4 : filled <= 64 ? 2 : 1);
-  int64_t splits = parts / found;
+  int64_t splits = 4 * found > 3 * parts ? 1 : (parts + found - 1) / found;
   if (splits > tiles / 2) splits = tiles / 2;
   if (splits < 1) splits = 1;
   p.per = (int)((tiles + splits - 1) / splits);
