@@ -100,7 +100,7 @@ __device__ __forceinline__ int value_swizzle(int r, int c) {
 // A block of rows: rows row0 .. row0 + block rows - 1 of the `rows` of sequence b, whose
 // first token is `start`; tokens first .. last of it.
 struct Block {
-  int b, start, tokens, row0, rows;
+  int b, start, tokens, keys, row0, rows;
   int begin, end;  // keys that some row of the block sees (begin rounded down to 16)
   int lowest;      // the first of them
   int place0;      // place of the sequence's first token among the keys
@@ -112,28 +112,33 @@ __device__ __forceinline__ int start_of(const PromptArgs &a, int b) { return min
 // Finds block `number` of the batch; false if the number is not used.
 __device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, int tile, Block &k) {
   const int lane = threadIdx.x & 63, group = a.Hq / a.Hkv;
-  // the last sequence whose numbers start at `number` or before, 64 candidates at a time
+  // The last sequence whose numbers start at `number` or before, 64 candidates at a time; each
+  // lane reads all that its candidate needs at once, so that one read follows the other only
+  // where there are more than 64 sequences.
   int low = 0, high = a.B;
-  while (high - low > 1 || low == 0) {
-    const int step = (high - low + 63) / 64, b = low + lane * step;
-    const bool before = b < high && first_block(start_of(a, min(b, a.B - 1)), b, group) <= number;
-    const int count = __popcll(__ballot(before));
+  for (;;) {
+    const int step = (high - low + 63) / 64, b = low + lane * step, at = min(b, a.B - 1);
+    const int start = start_of(a, at), next = start_of(a, at + 1);
+    const int length = a.block_table ? min(max(a.seq_lens[at], 0), a.max_len) : 0;
+    const int count = __popcll(__ballot(b < high && first_block(start, b, group) <= number));
     if (count == 0) return false;
-    low += (count - 1) * step;
+    if (step == 1) {
+      k.b = uniform(low + count - 1);
+      k.start = from_lane(start, count - 1);
+      k.tokens = from_lane(next, count - 1) - k.start;
+      k.keys = a.block_table ? from_lane(length, count - 1) : k.tokens;
+      break;
+    }
+    low = uniform(low + (count - 1) * step);
     high = min(high, low + step);
-    if (step == 1) break;
   }
-  k.b = uniform(low);
-  k.start = uniform(start_of(a, k.b));
-  k.tokens = uniform(start_of(a, k.b + 1)) - k.start;
   const int64_t row0 = (number - first_block(k.start, k.b, group)) * kBlockRows;
   if (k.tokens <= 0 || row0 < 0 || row0 >= (int64_t)k.tokens * group) return false;
   k.row0 = uniform((int)row0);
   k.rows = k.tokens * group;
   const int first = k.row0 / group, last = min(k.row0 + kBlockRows, k.rows) - 1;
-  const int keys = a.block_table ? uniform(min(max(a.seq_lens[k.b], 0), a.max_len)) : k.tokens;
-  k.place0 = keys - k.tokens;
-  k.end = a.causal ? max(0, k.place0 + last / group + 1) : keys;
+  k.place0 = k.keys - k.tokens;
+  k.end = a.causal ? max(0, k.place0 + last / group + 1) : k.keys;
   k.lowest = a.window > 0 ? max(0, k.place0 + first - a.window + 1) : 0;
   k.begin = k.lowest & ~15;
   k.tiles = (max(0, k.end - k.begin) + tile - 1) / tile;
@@ -231,7 +236,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   if (threadIdx.x < 2) lds_any[threadIdx.x] = 0;  // (before the first barrier)
 
   v8bf qf[kHeld];
-  {
+  auto load_queries = [&]() FP8LIN_INLINE {
     const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head;
     const int first = kFp8 && few ? 16 * h : 8 * h, odd_step = kFp8 && few ? 8 : 16;  // few_key_frags' order, or key_frag's
     // the weights' exponents grow with the scores: a negative scale turns the queries over
@@ -245,7 +250,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       else
         lds_q[((s - kHeld) * WAVES + wave) * 64 + lane] = __builtin_bit_cast(uint4, f);
     }
-  }
+  };
   auto query = [&](int s) FP8LIN_INLINE {
     return s < kHeld ? qf[s] : __builtin_bit_cast(v8bf, lds_q[((s - kHeld) * WAVES + wave) * 64 + lane]);
   };
@@ -597,7 +602,10 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       if (working && mine < any_end && mine + kMine > any_low)
         use_tile(subs, mine, lk, lv, ls + 32 * half, ls + KT + 32 * half, mine + kMine > all_end || mine < all_low, odd);
     };
-    if (tile0 < tile_end) fetch(tile0, lds_k0, lds_v0);
+    if (tile0 < tile_end) {
+      fetch(tile0, lds_k0, lds_v0);
+      load_queries();
+    }
     for (int t = tile0; t < tile_end; t += 2) {
       step(t, std::false_type{});
       if (t + 1 < tile_end) step(t + 1, std::true_type{});
@@ -763,6 +771,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     };
     if (wave >= tiles) return;
     fetch(0, lds_k0, lds_v0, lds_s0);
+    load_queries();
     for (int i = 0; wave + kFewWaves * i < tiles; i += 2) {
       step(i, std::false_type{});
       if (wave + kFewWaves * (i + 1) < tiles) step(i + 1, std::true_type{});
@@ -854,55 +863,58 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   }
 }
 
-// Joins the parts of divided blocks, in order: a wave takes a row.
+// Joins the parts of divided blocks, in order: D / 4 lanes take a row, kJoinRows rows a
+// workgroup.
+template <int D>
+constexpr int kJoinRows = 256 / (D / 4);
 template <int D>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPlan plan, const float *part) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
   const int group = a.Hq / a.Hkv;
   const int64_t number = blockIdx.x / (unsigned)a.Hkv;  // few blocks are divided: one launch
   const int kvh = (int)(blockIdx.x % (unsigned)a.Hkv);
+  const int d = (int)(threadIdx.x % (D / 4)) * 4;
   Block blk;
   if (!find_block(a, number, tile_keys(D), blk) || blk.tiles <= plan.per) return;
   const int parts = (blk.tiles + plan.per - 1) / plan.per;
-  constexpr size_t floats = prompt_part_floats(D);
-  const float *base = part + (number * a.Hkv + kvh) * plan.splits * (int64_t)floats;
-  for (int r = blockIdx.y * 4 + wave; r < min(kBlockRows, blk.rows - blk.row0); r += 4 * gridDim.y) {
-    float top = -INFINITY, l = 0.f, o[E] = {};
-    for (int k0 = 0; k0 < parts; k0 += 8) {  // eight parts in flight
-      float mp[8], lp[8], op[8][E];
+  constexpr int floats = prompt_part_floats(D);
+  const float *base = part + (number * a.Hkv + kvh) * plan.splits * floats;
+  const int filled = min(kBlockRows, blk.rows - blk.row0);
+  for (int r = (int)(blockIdx.y * kJoinRows<D> + threadIdx.x / (D / 4)); r < filled; r += (int)gridDim.y * kJoinRows<D>) {
+    float top = -INFINITY, l = 0.f, o[4] = {};
+    for (int k0 = 0; k0 < parts; k0 += 4) {  // four parts in flight
+      float mp[4], lp[4];
+      float4 op[4];
 #pragma unroll
-      for (int u = 0; u < 8; u++) {
-        const float *p = base + (size_t)min(k0 + u, parts - 1) * floats;
+      for (int u = 0; u < 4; u++) {
+        const float *p = base + (int64_t)min(k0 + u, parts - 1) * floats;
         mp[u] = p[kBlockRows * D + r];
         lp[u] = p[kBlockRows * (D + 1) + r];
-#pragma unroll
-        for (int e = 0; e < E; e++) op[u][e] = p[r * D + E * lane + e];
+        op[u] = *reinterpret_cast<const float4 *>(p + r * D + d);
       }
-      float high = top;
-#pragma unroll
-      for (int u = 0; u < 8; u++) high = fmaxf(high, mp[u]);
+      const float high = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])), top);
       const float shrink = top == high ? 1.f : __builtin_amdgcn_exp2f(top - high);
       top = high;
       l *= shrink;
 #pragma unroll
-      for (int e = 0; e < E; e++) o[e] *= shrink;
+      for (int e = 0; e < 4; e++) o[e] *= shrink;
 #pragma unroll
-      for (int u = 0; u < 8; u++) {
+      for (int u = 0; u < 4; u++) {
         if (k0 + u < parts) {
           const float f = mp[u] == top ? 1.f : __builtin_amdgcn_exp2f(mp[u] - top);
           l += lp[u] * f;
-#pragma unroll
-          for (int e = 0; e < E; e++) o[e] += op[u][e] * f;
+          o[0] += op[u].x * f;
+          o[1] += op[u].y * f;
+          o[2] += op[u].z * f;
+          o[3] += op[u].w * f;
         }
       }
     }
     const int row = blk.row0 + r;
     const int64_t out = (int64_t)(blk.start + row / group) * a.Hq + kvh * group + row % group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; e++) a.o[out * D + E * lane + e] = (uint16_t)f32_to_bf16_rne(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
+    *reinterpret_cast<uint2 *>(a.o + out * D + d) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
   }
 }
 
@@ -916,7 +928,9 @@ hipError_t launch(const PromptArgs &a, const PromptPlan &p, float *part, hipStre
     hipLaunchKernelGGL((prompt_kernel<D, SRC, CAP>), grid, dim3(64 * kBlockWaves), 0, stream, a, q, part);
   }
   if (p.splits > 1) {
-    const unsigned y = kBlockRows / 16;
+    // four passes each where there are many: workgroups that only look their block up take longer than they save
+    const int rows = kJoinRows<D> * ((int64_t)p.blocks * a.Hkv * p.filled > 1024 * kJoinRows<D> ? 4 : 1);
+    const unsigned y = (unsigned)((p.filled + rows - 1) / rows);
     hipLaunchKernelGGL((prompt_join_kernel<D>), dim3((unsigned)p.blocks * (unsigned)a.Hkv, y), dim3(256), 0, stream, a, p,
                        (const float *)part);
   }

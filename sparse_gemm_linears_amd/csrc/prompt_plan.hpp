@@ -20,6 +20,7 @@ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
 struct PromptPlan {
   int splits, per;
   int blocks;
+  int filled;  // rows of a block, on average
   int first;  // workgroup of the whole grid that a launch begins at
 };
 
@@ -33,7 +34,7 @@ __host__ __device__ inline int64_t first_block(int64_t start, int64_t b, int gro
 }
 
 // Partials of one part of a block: o [kBlockRows][D], then m and l [kBlockRows] each.
-__host__ __device__ constexpr size_t prompt_part_floats(int D) { return (size_t)kBlockRows * (D + 2); }
+__host__ __device__ constexpr int prompt_part_floats(int D) { return kBlockRows * (D + 2); }
 
 inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   const int group = a.Hq / a.Hkv;
@@ -45,12 +46,35 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   if (a.window > 0 && keys > seen) keys = seen;
   const int tile = tile_keys(a.D);
   const int64_t tiles = keys <= tile ? 1 : (keys + tile - 1) / tile;
-  const int64_t resident = (int64_t)cus * 2, found = (int64_t)p.blocks * a.Hkv;
-  const int64_t filled = rows / p.blocks;  // rows of a block
-  const int64_t parts = resident * (filled <= 32 ? 4 : filled <= 64 ? 2 : 1);
-  int64_t splits = 4 * found > 3 * parts ? 1 : (parts + found - 1) / found;
-  if (splits > tiles / 2) splits = tiles / 2;
-  if (splits < 1) splits = 1;
+  const int64_t found = (int64_t)p.blocks * a.Hkv;
+  p.filled = rows <= p.blocks ? 1 : (int)(rows / p.blocks);
+  int64_t splits = 1;
+  if (p.filled <= 64) {
+    // Small blocks are bound by the cache's bytes and by a workgroup's start; lengths differ, and what
+    // is cut evens them out.  (32 sequences of 5 to 8192 tokens, 16 rows each in e4m3: in 2, 4, 7, 8,
+    // 11, 14 parts 86, 87, 66, 76, 70, 70 us)
+    splits = (int64_t)2 * cus * (p.filled <= 32 ? 4 : 2) / found;
+    if (splits > tiles / 2) splits = tiles / 2;
+    if (splits < 1) splits = 1;
+  } else {
+    // Large blocks: a tile takes a workgroup that has its compute unit alone about half the time
+    // that it takes two that share one; a part costs its start and its partials, and any division
+    // the second kernel.  (In us, 32 / 8 heads of 128: 512 tokens over 4096 70 whole, 56 in 4 parts;
+    // prompts of 500 and of 1000 tokens 22 and 36 in 4 and 2 parts.)
+    const int64_t real = a.B == 1 ? (rows + kBlockRows - 1) / kBlockRows : rows / kBlockRows + (a.B + 1) / 2;
+    const double alone = a.D == 64 ? 0.9 : 1.1, pair = a.D == 64 ? 1.4 : a.D == 128 ? 2.1 : 2.3;
+    double best = 0;
+    for (int64_t s = 1; s <= 16 && s <= tiles; s++) {
+      const int64_t per = (tiles + s - 1) / s, parts = real * a.Hkv * s;
+      const int64_t rounds = parts <= cus ? 1 : (parts + 2 * cus - 1) / (2 * cus);
+      double us = rounds * (5 + per * (parts <= cus ? alone : pair));
+      if (s > 1) us += 8 + parts * p.filled * (a.D + 2) * 8 / 3e6;
+      if (s == 1 || us < best) {
+        best = us;
+        splits = s;
+      }
+    }
+  }
   p.per = (int)((tiles + splits - 1) / splits);
   p.splits = (int)((tiles + p.per - 1) / p.per);
   return p;
