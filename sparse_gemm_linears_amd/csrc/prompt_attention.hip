@@ -63,6 +63,13 @@ __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
 
 #define FP8LIN_INLINE __attribute__((always_inline))
 
+// The same address, which stays on the scalar side: lanes add 32-bit offsets to it.
+__device__ __forceinline__ const char *scalar(const char *p) {
+  uint64_t x = reinterpret_cast<uint64_t>(p);
+  asm volatile("" : "+s"(x));
+  return reinterpret_cast<const char *>(x);
+}
+
 // The same value, of which the compiler knows nothing: what is computed from it in a path that is
 // rarely taken is not computed ahead of the loop, where it would hold registers.
 __device__ __forceinline__ int opaque(int x) {
@@ -276,10 +283,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       found = ((int64_t)page * a.Hkv + kvh) * a.page_size + (key - p * a.page_size);
     }
   };
-  // line (in a cache) or token of the first key of run `run` of the tile at key0
-  auto run_line = [&](int key0, int run) FP8LIN_INLINE -> int64_t {
-    return kPaged ? from_lane(found, (key0 - found_from) / 16 + run) : (int64_t)blk.start + key0 + 16 * run;
-  };
+  // line in the cache of the first key of run `run` of the tile at key0
+  auto run_line = [&](int key0, int run) FP8LIN_INLINE { return from_lane(found, (key0 - found_from) / 16 + run); };
   const int64_t k_line = kPaged ? D * kBytes : a.k_token * 2, v_line = kPaged ? D * kBytes : a.v_token * 2;
   const char *k_base = static_cast<const char *>(a.k) + (kPaged ? 0 : (int64_t)kvh * a.k_head * 2);
   const char *v_base = static_cast<const char *>(a.v) + (kPaged ? 0 : (int64_t)kvh * a.v_head * 2);
@@ -295,6 +300,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   constexpr int kStep = kCopyRows * WAVES;
   constexpr int kKinds = kStep % 16 == 0 ? 1 : 16 / kStep < kCopiesPer ? 16 / kStep : kCopiesPer;
   auto copy_row = [&](int i) FP8LIN_INLINE { return i * kStep + wave * kCopyRows; };
+  auto copy_run = [&](int i) FP8LIN_INLINE { return i * kStep / 16 + (kStep > 16 ? wave * kCopyRows / 16 : 0); };
   uint32_t k_off[kKinds], v_off[kKinds];
   auto offsets = [&](int r, int c, int src, uint32_t &ko, uint32_t &vo) FP8LIN_INLINE {
     ko = (uint32_t)((src & 15) * (int)k_line + 16 * (kFp8 ? c : key_swizzle<D>(r, c)));
@@ -308,8 +314,10 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   // e4m3 codes go through registers: 16 codes of a lane become 32 bytes of bf16
   uint4 raw_k[kFp8 ? kCopiesPer : 1], raw_v[kFp8 ? kCopiesPer : 1];
   float raw_s[2];
-  auto copy_rows = [&](int i, int64_t line, uint32_t ko, uint32_t vo, uint8_t *lk, uint8_t *lv) FP8LIN_INLINE {
-    const char *kp = k_base + line * k_line + ko, *vp = v_base + line * v_line + vo;
+  // kt, vt: the lines of the first row's run
+  auto copy_rows = [&](int i, const char *kt, const char *vt, uint32_t ko, uint32_t vo, uint8_t *lk,
+                       uint8_t *lv) FP8LIN_INLINE {
+    const char *kp = scalar(kt) + ko, *vp = scalar(vt) + vo;
     if constexpr (kFp8) {
       raw_k[i] = *reinterpret_cast<const uint4 *>(kp);
       raw_v[i] = *reinterpret_cast<const uint4 *>(vp);
@@ -323,6 +331,14 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     if constexpr (kPaged) {
       if (t == tile0 || key0 + KT > found_from + 1024) look_up(key0);
     }
+    const char *kt = k_base, *vt = v_base;  // the tile's lines, of rows
+    const int64_t k_run16 = 16 * k_line, v_run16 = 16 * v_line;
+    if constexpr (!kPaged) {
+      kt += (int64_t)(blk.start + key0) * k_line;
+      vt += (int64_t)(blk.start + key0) * v_line;
+    }
+    auto k_run = [&](int run) FP8LIN_INLINE { return kt + (kPaged ? run_line(key0, run) * kLine : run * k_run16); };
+    auto v_run = [&](int run) FP8LIN_INLINE { return vt + (kPaged ? run_line(key0, run) * kLine : run * v_run16); };
     if (whole(key0)) {
 #pragma unroll
       for (int i = 0; i < kCopiesPer; i++) {
@@ -332,7 +348,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
           const int self = opaque(lane), r = copy_row(i) + self / kLanes;
           offsets(r, self % kLanes, r, ko, vo);
         }
-        copy_rows(i, run_line(key0, copy_row(i) >> 4), ko, vo, lk, lv);
+        const int run = copy_run(i);
+        copy_rows(i, k_run(run), v_run(run), ko, vo, lk, lv);
       }
     } else {
 #pragma unroll
@@ -341,7 +358,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
         const int self = opaque(lane), r = copy_row(i) + self / kLanes;
         uint32_t ko, vo;
         offsets(r, self % kLanes, near(key0, r), ko, vo);
-        copy_rows(i, run_line(key0, uniform(near(key0, copy_row(i))) >> 4), ko, vo, lk, lv);
+        const int run = uniform(near(key0, copy_row(i))) >> 4;
+        copy_rows(i, k_run(run), v_run(run), ko, vo, lk, lv);
       }
     }
     if constexpr (kFp8) {  // the scales: the first wave those of the keys, the last those of the values
@@ -654,7 +672,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
           run = uniform(near(key0, r0)) >> 4;
           at = (uint32_t)((src & 15) * (int)line + 16 * (place(keys, rl, cl) ^ flip));
         }
-        copy16_global_to_lds(base + line_of(run) * line + at, to + wave * kFewTile + r0 * kLine);
+        copy16_global_to_lds(scalar(base + line_of(run) * line) + at, to + wave * kFewTile + r0 * kLine);
       };
 #pragma unroll
       for (int j = 0; j < kFewCopies; j++) copy(std::true_type{}, j, k_base, k_line, lk);

@@ -57,18 +57,22 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     if (splits > tiles / 2) splits = tiles / 2;
     if (splits < 1) splits = 1;
   } else {
-    // Large blocks: a tile takes a workgroup that has its compute unit alone about half the time
+    // Large blocks: a tile takes a workgroup that has its compute unit alone about 0.7 of the time
     // that it takes two that share one; a part costs its start and its partials, and any division
     // the second kernel.  (In us, 32 / 8 heads of 128: 512 tokens over 4096 70 whole, 56 in 4 parts;
-    // prompts of 500 and of 1000 tokens 22 and 36 in 4 and 2 parts.)
+    // prompts of 500 and of 1000 tokens
+    // 22 and 36 in 4 and 2 parts, 18 and 30 whole.)
     const int64_t real = a.B == 1 ? (rows + kBlockRows - 1) / kBlockRows : rows / kBlockRows + (a.B + 1) / 2;
-    const double alone = a.D == 64 ? 0.9 : 1.1, pair = a.D == 64 ? 1.4 : a.D == 128 ? 2.1 : 2.3;
+    const double codes = a.k_scale ? 1.5 : 1.0;
+    const double alone = codes * (a.D == 64 ? 0.9 : 1.5), pair = codes * (a.D == 64 ? 1.4 : a.D == 128 ? 2.1 : 2.3);
+    // (of packed prompts only the sum of their lengths is known: twice the mean stands for the longest)
+    const int64_t mean = 2 * (int64_t)a.T / a.B / tile + 1, usual = a.block_table || tiles < mean ? tiles : mean;
     double best = 0;
-    for (int64_t s = 1; s <= 16 && s <= tiles; s++) {
-      const int64_t per = (tiles + s - 1) / s, parts = real * a.Hkv * s;
+    for (int64_t s = 1; s <= 64 && s <= tiles; s++) {
+      const int64_t per = (usual + s - 1) / s, parts = real * a.Hkv * s;
       const int64_t rounds = parts <= cus ? 1 : (parts + 2 * cus - 1) / (2 * cus);
       double us = rounds * (5 + per * (parts <= cus ? alone : pair));
-      if (s > 1) us += 8 + parts * p.filled * (a.D + 2) * 8 / 3e6;
+      if (s > 1) us += 8 + s * 0.25 + parts * p.filled * (a.D + 2) * 8 / 8e6;
       if (s == 1 || us < best) {
         best = us;
         splits = s;
