@@ -68,7 +68,8 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     // (of packed prompts only the sum of their lengths is known: twice the mean stands for the longest)
     const int64_t mean = 2 * (int64_t)a.T / a.B / tile + 1, usual = a.block_table || tiles < mean ? tiles : mean;
     double best = 0;
-    for (int64_t s = 1; s <= 64 && s <= tiles; s++) {
+    // (no division makes more than eight workgroups a compute unit: its partials stay below 300 MB)
+    for (int64_t s = 1; s == 1 || (s <= 64 && s <= tiles && s * found <= 8 * cus); s++) {
       const int64_t per = (usual + s - 1) / s, parts = real * a.Hkv * s;
       const int64_t rounds = parts <= cus ? 1 : (parts + 2 * cus - 1) / (2 * cus);
       double us = rounds * (5 + per * (parts <= cus ? alone : pair));
