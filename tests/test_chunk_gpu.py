@@ -150,7 +150,8 @@ def test_bad_pages_are_clamped(gpu_lib):
     lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
     want = gpu_lib.paged_chunk_attention(q.cuda(), *cache, table, lens_, starts_of(new))
     bad = table.clone()
-    bad[1] = torch.tensor([-1, 1 << 30, -(1 << 31), (1 << 31) - 1] * 2, dtype=torch.int32, device="cuda")[: bad.shape[1]]
+    wild = torch.tensor([-1, 1 << 30, -(1 << 31), (1 << 31) - 1] * 2, dtype=torch.int32, device="cuda")
+    bad[1] = wild[: bad.shape[1]]
     got = gpu_lib.paged_chunk_attention(q.cuda(), *cache, bad, lens_, starts_of(new))
     assert torch.equal(got[:3], want[:3]) and torch.equal(got[23:], want[23:])
 
@@ -210,3 +211,109 @@ def test_binding_refusals(gpu_lib):
     for bad in (dict(max_len=10 ** 6), dict(max_len=-1), dict(window=-1), dict(scale=float("inf")), dict(softcap=-1.0)):
         with pytest.raises(gpu_lib.Fp8LinError):
             f(q, *cache, table, lens, starts, **bad)
+
+
+def shared_pages(D, Hkv, length, page, fp8, seed):
+    """A cache of one sequence of `length` tokens and its table's row: (cache, row, keys, values in 64 bits)."""
+    dev, table, live = paged(gen("shared pages", seed), [length], Hkv, D, page, fp8, 0)
+    return dev, table[0], live[0]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,new,length,Hq,Hkv,D,page", [
+    (300, 1, 4500, 16, 8, 64, 32), (160, 3, 4500, 16, 8, 128, 16), (90, 1, 2300, 16, 16, 256, 64),
+    (40, 130, 2300, 8, 4, 128, 48), (70, 40, 1100, 4, 2, 64, 16)])
+def test_many_sequences_without_division(gpu_lib, B, new, length, Hq, Hkv, D, page, fp8):
+    """Batches that fill the device, so that a workgroup goes over a whole cache (and looks its pages up again and
+    again).  The sequences share their pages and stand at other lengths; a few of them are checked."""
+    cache, row, (k, v) = shared_pages(D, Hkv, length, page, fp8, B)
+    r = gen("filling", B)
+    lens = [length - (b * 37) % 200 for b in range(B)]
+    q = ref.bf16(1.5 * r.standard_normal((B * new, Hq, D)))
+    table = row.expand(B, -1).contiguous()
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    call = gpu_lib.paged_chunk_attention_fp8 if fp8 else gpu_lib.paged_chunk_attention
+    o, lse = call(q.cuda(), *cache, table, lens_, starts_of([new] * B), return_lse=True)
+    check = Check(D ** -0.5, 0.0)
+    for b in (0, 1, B // 2, B - 1):
+        rows, n = slice(b * new, (b + 1) * new), lens[b]
+        check.sequence(o[rows], lse[rows], ref.f64(q[rows]), k[:, :n], v[:, :n], n - new, what=f"of sequence {b}")
+    check.done()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_lines_past_32_bits(gpu_lib, fp8):
+    """A cache of more than 2^32 values, its last pages used: offsets that do not fit 32 bits."""
+    pages = (1 << 32) // (16 * 8 * 128) + 300
+    chunk_case(gpu_lib, [3, 90], [50, 133], 16, 8, 128, 16, fp8, pages=pages)
+
+
+def test_searches_of_many_sequences(gpu_lib):
+    """More sequences than one search round of 64 and of 4096 finds, most of them without tokens."""
+    for B in (65, 5000):
+        new = [0] * B
+        for b in (0, 1, 63, 64, B // 2, B - 1):
+            new[b] = 1 + b % 3
+        cache, row, (k, v) = shared_pages(64, 1, 40, 16, False, B)
+        q = ref.bf16(gen("search", B).standard_normal((sum(new), 2, 64)))
+        lens = torch.full((B,), 40, dtype=torch.int32, device="cuda")
+        o, lse = gpu_lib.paged_chunk_attention(q.cuda(), *cache, row.expand(B, -1).contiguous(), lens, starts_of(new),
+                                               return_lse=True)
+        check, at = Check(64 ** -0.5, 0.0), 0
+        for b, n in enumerate(new):
+            if n:
+                rows = slice(at, at + n)
+                check.sequence(o[rows], lse[rows], ref.f64(q[rows]), k, v, 40 - n, what=f"of sequence {b}")
+            at += n
+        check.done()
+
+
+def test_unordered_starts_stay_in_bounds(gpu_lib):
+    """Starts that fall, or lie outside the rows: their sequences' rows are unspecified, and a sequence beside them
+    whose rows no other one claims keeps its results where it is found."""
+    new, lens = [4, 4, 4], [30, 40, 50]
+    q, cache, table, _ = chunk_inputs(new, lens, 2, 1, 64, 16, False)
+    lens_ = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for bad in ([0, 9, 3, 12], [-5, 4, 8, 400], [12, 8, 4, 0], [1 << 30, -(1 << 31), (1 << 31) - 1, 5]):
+        starts = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        o = torch.zeros(14, 2, 64, dtype=torch.bfloat16, device="cuda")  # two rows more than there are
+        gpu_lib.paged_chunk_attention(q.cuda(), *cache, table, lens_, starts, o=o[:12])
+        gpu_lib.prompt_attention(q.cuda(), q[:, :1].cuda(), q[:, :1].cuda(), starts, o=o[:12])
+        torch.cuda.synchronize()
+        assert (o[12:] == 0).all()
+
+
+def test_two_streams_and_two_graphs(gpu_lib):
+    """Divided calls at once on two streams, and two graphs of such calls replayed in turn: each has scratch memory of
+    its own."""
+    cases = []
+    for i, (new, lens) in enumerate((([4, 2], [900, 3000]), ([40], [2500]))):
+        q, cache, table, _ = chunk_inputs(new, lens, 8, 2, 128, 16, bool(i))
+        call = gpu_lib.paged_chunk_attention_fp8 if i else gpu_lib.paged_chunk_attention
+        args = (q.cuda(), *cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), starts_of(new))
+        cases.append((call, args, call(*args), torch.empty_like(args[0])))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for s, (call, args, _, o) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                call(*args, o=o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, o) for _, _, want, o in cases)
+    graphs = []
+    for s, (call, args, _, o) in zip(streams, cases):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call(*args, o=o)
+        graphs.append(g)
+    for _ in range(3):
+        for _, _, _, o in cases:
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want, o) for _, _, want, o in cases)
+        for call, args, want, _ in cases:  # eager work between the replays
+            assert torch.equal(call(*args), want)

@@ -132,6 +132,27 @@ def test_strided_views(gpu_lib):
     assert ((ref_o.float() - one.float()).abs().max() < 2.0 ** -5).item()
 
 
+def test_strides_past_32_bits(gpu_lib):
+    """Tokens so far apart that their offsets do not fit 32 bits."""
+    T, D = 2100, 64
+    wide = torch.empty(T, 1 << 20, dtype=torch.bfloat16, device="cuda")  # 2^31 values and more
+    q, k, v = (t.cuda() for t in inputs([T], 2, 1, D))
+    views = []
+    for i, t in enumerate((q, k, v)):
+        at = wide[:, i << 10 : (i << 10) + t.shape[1] * D].view(T, t.shape[1], D)
+        at.copy_(t)
+        views.append(at)
+    want = gpu_lib.prompt_attention(q, k, v, starts_of([T]))
+    assert torch.equal(gpu_lib.prompt_attention(*views, starts_of([T])), want)
+
+
+def test_prompts_of_falling_and_rising_lengths(gpu_lib):
+    """Up to 64 prompts begin with their longest rows first, whatever their order."""
+    lens = [int(x) for x in 2 ** gen("order").uniform(0, 9.5, 64)]
+    for order in (sorted(lens), sorted(lens, reverse=True), lens, lens[:63] + [0], [0] * 63 + [130], lens + [7, 700]):
+        prompt_case(gpu_lib, order, 4, 2, 64)
+
+
 def test_rows_outside_every_prompt_stay(gpu_lib):
     lens, Hq, Hkv, D = [33, 0, 100], 4, 2, 64
     q, k, v = (t.cuda() for t in inputs(lens, Hq, Hkv, D, extra=30))
@@ -166,7 +187,8 @@ def test_hidden_values_do_not_reach_a_row(gpu_lib):
                     assert torch.equal(lse[~sees], want_lse[~sees])
                     err = (o[~sees].float() - want[~sees].float()).abs()
                     # one key at a time adds its products in another order
-                    assert (err <= 2.0 ** -7 * want[~sees].float().abs() + 2.0 ** -16).all(), (D, window, bad, at, where)
+                    within = err <= 2.0 ** -7 * want[~sees].float().abs() + 2.0 ** -16
+                    assert within.all(), (D, window, bad, at, where)
                     if where == "v":
                         assert not torch.isfinite(o[sees][..., 5::7]).any()
                         assert torch.isfinite(o[sees][..., 4::7]).all()
