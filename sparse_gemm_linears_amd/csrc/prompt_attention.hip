@@ -197,6 +197,97 @@ __device__ __forceinline__ bool find_ranked(const PromptArgs &a, int rank, int t
   return true;
 }
 
+// A workgroup's part of a block.
+struct Part {
+  int per;       // tiles of a part of its block
+  int split;     // which one it is
+  int splits;    // the most that there are
+  int64_t slot;  // place of the block's first part among the partials, and steps to the next one
+  int step;
+};
+
+// The part at `rank` of a key head's, where long sequences are divided most: into as many
+// parts as keep every one's cost below the least bound for which all parts are at most
+// plan.shares.  A tile of a block of at most 32 rows counts as two thirds of another one in e4m3
+// (which waits for the cache), and one and a half times as much in bf16.
+template <bool CODES>
+__device__ __forceinline__ bool find_share(const PromptArgs &a, const PromptPlan &plan, int rank, int kvh, int tile,
+                                           Block &k, Part &part) {
+  constexpr int kEach = kShareBatch / 64, kMost = 4096;  // (a valid batch has fewer blocks and parts)
+  const int lane = threadIdx.x & 63, group = a.Hq / a.Hkv, each = (a.B + 63) / 64;
+  int start[kEach], tokens[kEach], keys[kEach], blocks[kEach], cost[kEach];
+#pragma unroll
+  for (int j = 0; j < kEach; j++) {
+    const int b = lane * each + j, at = min(b, a.B - 1);
+    start[j] = tokens[j] = keys[j] = blocks[j] = cost[j] = 0;
+    if (j >= each) continue;
+    start[j] = start_of(a, at);
+    tokens[j] = start_of(a, at + 1) - start[j];
+    keys[j] = min(max(a.seq_lens[at], 0), a.max_len);
+    if (b >= a.B || tokens[j] <= 0) continue;
+    const int64_t rows = (int64_t)tokens[j] * group;
+    blocks[j] = (int)((rows + kBlockRows - 1) / kBlockRows);
+    const int seen = a.window > 0 ? min(keys[j], a.window + (kBlockRows + group - 1) / group + 15) : keys[j];
+    cost[j] = (seen + tile - 1) / tile * ((rows <= kWaveRows) == CODES ? 2 : 3);
+  }
+  auto parts_of = [&](int j, float inverse) FP8LIN_INLINE {
+    return min(max((int)__builtin_ceilf((float)cost[j] * inverse), 1), kMost);
+  };
+  auto count_of = [&](int j, float inverse) FP8LIN_INLINE { return min(min(blocks[j], kMost) * parts_of(j, inverse), 1 << 20); };
+  auto large = [&](int j) FP8LIN_INLINE { return tokens[j] * (int64_t)group > kWaveRows; };
+  auto mine_of = [&](float inverse, bool larges, bool others) FP8LIN_INLINE {
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; j++)
+      if (j < each && (large(j) ? larges : others)) mine += count_of(j, inverse);
+    return mine;
+  };
+  constexpr int kLeast = 6;  // two tiles
+  int bound = kLeast - 1;    // the largest that is too small
+  for (int bit = 1 << (31 - __builtin_clz(3 * plan.per | 1)); bit > 0; bit >>= 1)
+    if (wave_sum(mine_of(__builtin_amdgcn_rcpf((float)(bound + bit)), true, true)) > plan.shares) bound += bit;
+  const float inverse = __builtin_amdgcn_rcpf((float)(bound + 1));
+  const int mine_large = mine_of(inverse, true, false), all_large = wave_sum(mine_large);
+  const bool takes_large = rank < all_large;  // the blocks that take longest begin first
+  const int mine = takes_large ? mine_large : mine_of(inverse, false, true);
+  int before = mine;  // and of the lanes below
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int other = __shfl_up(before, d, 64);
+    if (lane >= d) before += other;
+  }
+  const int place = takes_large ? rank : rank - all_large;
+  const uint64_t behind = __ballot(before > place);
+  if (behind == 0) return false;
+  const int from = __ffsll((unsigned long long)behind) - 1;
+  int index = place - (from_lane(before, from) - from_lane(mine, from)), splits = 0, all = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; j++) {
+    const int count = from_lane(large(j) == takes_large ? count_of(j, inverse) : 0, from);
+    if (j < each && splits == 0) {
+      if (index < count) {
+        k.b = from * each + j;
+        k.start = from_lane(start[j], from);
+        k.tokens = from_lane(tokens[j], from);
+        k.keys = from_lane(keys[j], from);
+        splits = from_lane(parts_of(j, inverse), from);
+        all = from_lane(blocks[j], from);
+      } else {
+        index -= count;
+      }
+    }
+  }
+  const int behind_it = index / splits;  // blocks of the sequence: the last ones see the most keys
+  if (behind_it >= all) return false;
+  fill_block(a, (all - 1 - behind_it) * kBlockRows, tile, k);
+  part.split = index - behind_it * splits;
+  part.splits = splits;
+  part.per = max(1, (k.tiles + splits - 1) / splits);
+  part.slot = (int64_t)(rank - part.split) * a.Hkv + kvh;
+  part.step = a.Hkv;
+  return rank - part.split + splits <= plan.shares;  // (not so of starts that are out of order)
+}
+
 // tanh of each value.  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that would lose a
 // small score's low bits, its power series (2^-26 of it is left out).
 template <int N>
@@ -248,12 +339,17 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   const int group = a.Hq / a.Hkv;
   const uint32_t self = (uint32_t)plan.first + blockIdx.x, rest = self / (uint32_t)a.Hkv;
   const int kvh = (int)(self - rest * (uint32_t)a.Hkv);
-  const int split = (int)(rest % (uint32_t)plan.splits);
-  const int64_t number = plan.blocks - 1 - (int)(rest / (uint32_t)plan.splits);  // a sequence's longest rows first
   Block blk;
-  const bool ranked = !kPaged && a.causal && a.window == 0 && a.B > 1 && a.B <= 64 && plan.splits == 1;
-  if (!(ranked ? find_ranked(a, (int)rest, KT, blk) : find_block(a, number, KT, blk))) return;
-  const int tile0 = split * plan.per, tile_end = min(blk.tiles, tile0 + plan.per);
+  Part mine_part{};
+  if (kPaged && plan.shares > 0) {
+    if (!find_share<kFp8>(a, plan, (int)rest, kvh, KT, blk, mine_part)) return;
+  } else {
+    const int64_t number = plan.blocks - 1 - (int)(rest / (uint32_t)plan.splits);  // a sequence's longest rows first
+    const bool ranked = !kPaged && a.causal && a.window == 0 && a.B > 1 && a.B <= 64 && plan.splits == 1;
+    if (!(ranked ? find_ranked(a, (int)rest, KT, blk) : find_block(a, number, KT, blk))) return;
+    mine_part = Part{plan.per, (int)(rest % (uint32_t)plan.splits), plan.splits, (number * a.Hkv + kvh) * plan.splits, 1};
+  }
+  const int split = mine_part.split, tile0 = split * mine_part.per, tile_end = min(blk.tiles, tile0 + mine_part.per);
   if (split > 0 && tile0 >= blk.tiles) return;
 
   // Blocks of more than 64 rows: a wave takes 32 of them and all keys of a tile.  Of 33 to 64: two
@@ -895,7 +991,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   const int mine = wave_row + opaque(n);
   if (mine >= blk.rows) return;
   const int64_t out = (int64_t)(blk.start + mine / group) * a.Hq + kvh * group + mine % group;
-  if (blk.tiles <= plan.per) {
+  if (blk.tiles <= mine_part.per) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t *dst = a.o + out * D + 4 * h;
 #pragma unroll
@@ -907,7 +1003,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     }
     if (a.lse && h == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
   } else {
-    float *base = part + ((number * a.Hkv + kvh) * plan.splits + split) * (int64_t)prompt_part_floats(D);
+    float *base = part + (mine_part.slot + split * mine_part.step) * (int64_t)prompt_part_floats(D);
     const int r = mine - blk.row0;
 #pragma unroll
     for (int i = 0; i < D / 8; i++) {
@@ -933,12 +1029,25 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPl
   const int kvh = (int)(blockIdx.x % (unsigned)a.Hkv);
   const int d = (int)(threadIdx.x % (D / 4)) * 4;
   Block blk;
-  if (!find_block(a, number, tile_keys(D), blk) || blk.tiles <= plan.per) return;
-  const int parts = (blk.tiles + plan.per - 1) / plan.per;
-  constexpr int floats = prompt_part_floats(D);
-  const float *base = part + (number * a.Hkv + kvh) * plan.splits * floats;
+  Part from{};
+  // of shares the block's parts' workgroups take its rows in turn
+  int first = (int)blockIdx.y, stride = (int)gridDim.y;
+  if (plan.shares > 0) {
+    if (!(a.k_scale ? find_share<true>(a, plan, (int)number, kvh, tile_keys(D), blk, from)
+                    : find_share<false>(a, plan, (int)number, kvh, tile_keys(D), blk, from)))
+      return;
+    first = from.split * stride + first;
+    stride *= from.splits;
+  } else {
+    if (!find_block(a, number, tile_keys(D), blk)) return;
+    from = Part{plan.per, 0, plan.splits, (number * a.Hkv + kvh) * plan.splits, 1};
+  }
+  if (blk.tiles <= from.per) return;
+  const int parts = (blk.tiles + from.per - 1) / from.per;
+  const int64_t floats = (int64_t)from.step * prompt_part_floats(D);
+  const float *base = part + from.slot * prompt_part_floats(D);
   const int filled = min(kBlockRows, blk.rows - blk.row0);
-  for (int r = (int)(blockIdx.y * kJoinRows<D> + threadIdx.x / (D / 4)); r < filled; r += (int)gridDim.y * kJoinRows<D>) {
+  for (int r = first * kJoinRows<D> + (int)threadIdx.x / (D / 4); r < filled; r += stride * kJoinRows<D>) {
     float top = -INFINITY, l = 0.f, o[4] = {};
     for (int k0 = 0; k0 < parts; k0 += 4) {  // four parts in flight
       float mp[4], lp[4];
@@ -979,19 +1088,19 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPl
 
 template <int D, Source SRC, bool CAP>
 hipError_t launch(const PromptArgs &a, const PromptPlan &p, float *part, hipStream_t stream) {
-  const int64_t all = (int64_t)p.blocks * a.Hkv * p.splits;
+  const int64_t all = prompt_parts(p, a.Hkv);
   PromptPlan q = p;
   for (int64_t first = 0; first < all; first += kPromptGrid) {
     q.first = (int)first;
     const dim3 grid((unsigned)(all - first < kPromptGrid ? all - first : kPromptGrid));
     hipLaunchKernelGGL((prompt_kernel<D, SRC, CAP>), grid, dim3(64 * kBlockWaves), 0, stream, a, q, part);
   }
-  if (p.splits > 1) {
+  if (prompt_joins(p)) {
     // four passes each where there are many: workgroups that only look their block up take longer than they save
     const int rows = kJoinRows<D> * ((int64_t)p.blocks * a.Hkv * p.filled > 1024 * kJoinRows<D> ? 4 : 1);
-    const unsigned y = (unsigned)((p.filled + rows - 1) / rows);
-    hipLaunchKernelGGL((prompt_join_kernel<D>), dim3((unsigned)p.blocks * (unsigned)a.Hkv, y), dim3(256), 0, stream, a, p,
-                       (const float *)part);
+    const unsigned x = p.shares > 0 ? (unsigned)all : (unsigned)p.blocks * (unsigned)a.Hkv;
+    const unsigned y = p.shares > 0 ? (p.filled > kWaveRows ? 2 : 1) : (unsigned)((p.filled + rows - 1) / rows);
+    hipLaunchKernelGGL((prompt_join_kernel<D>), dim3(x, y), dim3(256), 0, stream, a, p, (const float *)part);
   }
   return hipGetLastError();
 }
@@ -1011,8 +1120,7 @@ hipError_t launch_dim(const PromptArgs &a, const PromptPlan &p, float *part, hip
 
 size_t prompt_partial_bytes(const PromptArgs &a, int cus) {
   const PromptPlan p = plan_prompt(a, cus);
-  return p.splits == 1 ? 0
-                       : (size_t)p.blocks * a.Hkv * p.splits * prompt_part_floats(a.D) * sizeof(float);
+  return prompt_joins(p) ? (size_t)prompt_parts(p, a.Hkv) * prompt_part_floats(a.D) * sizeof(float) : 0;
 }
 
 hipError_t launch_prompt_attention(const PromptArgs &a, float *part, hipStream_t stream) {

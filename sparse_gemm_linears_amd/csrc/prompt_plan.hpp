@@ -17,12 +17,18 @@ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
 // A block of kBlockRows rows of one sequence and key head is a workgroup, or `splits` of
 // them that take `per` key tiles each and leave partials.  Blocks are numbered through the
 // batch: sequence b has numbers first_block(b) .. first_block(b + 1) - 1, some unused.
+// With shares the blocks of the longest sequences are divided most: the kernel finds
+// from the lengths how, so that a key head has at most `shares` parts (`per` is then the number
+// of tiles that no block has more of).
 struct PromptPlan {
-  int splits, per;
+  int splits, per, shares;
   int blocks;
   int filled;  // rows of a block, on average
   int first;  // workgroup of the whole grid that a launch begins at
 };
+
+// Sequences of a batch that shares are made for: four a lane.
+constexpr int kShareBatch = 256;
 
 // Workgroups of one launch: a grid counts its threads in 32 bits.
 constexpr int kPromptGrid = 1 << 22;
@@ -35,6 +41,12 @@ __host__ __device__ inline int64_t first_block(int64_t start, int64_t b, int gro
 
 // Partials of one part of a block: o [kBlockRows][D], then m and l [kBlockRows] each.
 __host__ __device__ constexpr int prompt_part_floats(int D) { return kBlockRows * (D + 2); }
+
+// Workgroups of the attention, each of which may leave partials.
+inline int64_t prompt_parts(const PromptPlan &p, int Hkv) {
+  return (int64_t)Hkv * (p.shares > 0 ? p.shares : (int64_t)p.blocks * p.splits);
+}
+inline bool prompt_joins(const PromptPlan &p) { return p.splits > 1 || p.shares > 0; }
 
 inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   const int group = a.Hq / a.Hkv;
@@ -49,6 +61,18 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   const int64_t found = (int64_t)p.blocks * a.Hkv;
   p.filled = rows <= p.blocks ? 1 : (int)(rows / p.blocks);
   int64_t splits = 1;
+  if (a.block_table && a.B > 1 && a.B <= kShareBatch && found <= 8 * cus && tiles > 2) {
+    // As many parts as run at once, or twice or three times as many where there are more blocks: a few
+    // more than run at once take longest.  (32 sequences of 5 to 8192 tokens, 16 rows each, e4m3, 8 key
+    // heads: 64 parts a head 58 us, 72 70, 128 66, 192 75; of equal lengths 52 with 64, and 67 in 8 parts
+    // each.)  Where some blocks are large they come first, and small ones fill the end.  (512 tokens over 4096
+    // beside 23 single ones over 300 to 4096: 64 parts a head 113 us, 80 99, 96 108.)
+    const int64_t round = 2 * cus, rounds = (found + found / 4 + round - 1) / round;
+    p.shares = (int)(rounds * round * (p.filled > kWaveRows ? 5 : 4) / 4 / a.Hkv);
+    p.splits = 1;
+    p.per = (int)tiles;
+    return p;
+  }
   if (p.filled <= 64) {
     // Small blocks are bound by the cache's bytes and by a workgroup's start; lengths differ, and what
     // is cut evens them out.  (32 sequences of 5 to 8192 tokens, 16 rows each in e4m3: in 2, 4, 7, 8,

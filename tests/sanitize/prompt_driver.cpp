@@ -120,12 +120,14 @@ static void plans() {
                     if (window && seen < keys) keys = seen;
                     EXPECT(p.splits >= 1 && p.per >= 1 && p.blocks >= 1 && p.filled >= 1);
                     EXPECT((int64_t)p.splits * p.per * fp8lin::tile_keys(D) >= keys);
-                    EXPECT((int64_t)p.blocks * Hkv * p.splits < (int64_t(1) << 31));
+                    EXPECT(fp8lin::prompt_parts(p, a.Hkv) < (int64_t(1) << 31));
+                    // with shares every block has one at least
+                    EXPECT(p.shares == 0 || (p.shares >= p.blocks && p.splits == 1 && kind && B <= 256));
                     // the join is one launch
-                    EXPECT(p.splits == 1 || (int64_t)p.blocks * Hkv * 64 < int64_t(1) << 24);
-                    const size_t bytes = p.splits == 1 ? 0
-                                                       : (size_t)p.blocks * Hkv * p.splits *
-                                                             fp8lin::prompt_part_floats(D) * sizeof(float);
+                    EXPECT(!fp8lin::prompt_joins(p) || fp8lin::prompt_parts(p, a.Hkv) * 256 < int64_t(1) << 22);
+                    const size_t bytes = !fp8lin::prompt_joins(p) ? 0
+                                                                  : (size_t)fp8lin::prompt_parts(p, a.Hkv) *
+                                                                        fp8lin::prompt_part_floats(D) * sizeof(float);
                     worst = bytes > worst ? bytes : worst;
                     EXPECT(bytes < size_t(1) << 30);
                     checked++;

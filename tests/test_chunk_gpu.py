@@ -268,6 +268,38 @@ def test_searches_of_many_sequences(gpu_lib):
         check.done()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,D,Hkv,group,window", [(2, 128, 2, 4, 0), (63, 64, 1, 2, 0), (65, 128, 1, 16, 0),
+                                                  (130, 64, 1, 3, 100), (256, 128, 1, 1, 0), (257, 64, 1, 1, 0),
+                                                  (9, 256, 2, 2, 0), (24, 128, 3, 5, 300)])
+def test_shares_of_ragged_sequences(gpu_lib, B, D, Hkv, group, window, fp8):
+    """Batches of sequences from no key to thousands, single tokens beside long chunks and beside none, divided by
+    their lengths."""
+    cache, row, (k, v) = shared_pages(D, Hkv, 4096, 32, fp8, B)
+    r = gen("shares", B, D)
+    lens = [int(4096 ** x) for x in r.random(B)]
+    new = [int(x) for x in r.integers(0, 4, B)]
+    for b in (0, B // 2, B - 1):  # long ones, a chunk, and an empty one
+        lens[b], new[b] = 4096 - b % 7, 1 + 70 * (b == B // 2)
+    lens[B // 3], new[B // 3] = (0, 2) if B > 3 else (4096, 1)
+    q = ref.bf16(1.5 * r.standard_normal((sum(new), Hkv * group, D)))
+    call = gpu_lib.paged_chunk_attention_fp8 if fp8 else gpu_lib.paged_chunk_attention
+    table = row.expand(B, -1).contiguous()
+    o, lse = call(q.cuda(), *cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), starts_of(new),
+                  window=window, return_lse=True)
+    check, at = Check(D ** -0.5, 0.0), 0
+    for b, n in enumerate(new):
+        rows = slice(at, at + n)
+        if n and (lens[b] > 2000 or b % 5 == 0 or n > lens[b]):
+            check.sequence(o[rows], lse[rows], ref.f64(q[rows]), k[:, : lens[b]], v[:, : lens[b]], lens[b] - n,
+                           window, what=f"of sequence {b}")
+        at += n
+    check.done()
+    again = call(q.cuda(), *cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), starts_of(new),
+                 window=window)
+    assert torch.equal(again, o)  # no order of the parts changes a result
+
+
 def test_unordered_starts_stay_in_bounds(gpu_lib):
     """Starts that fall, or lie outside the rows: their sequences' rows are unspecified, and a sequence beside them
     whose rows no other one claims keeps its results where it is found."""
@@ -281,6 +313,22 @@ def test_unordered_starts_stay_in_bounds(gpu_lib):
         gpu_lib.prompt_attention(q.cuda(), q[:, :1].cuda(), q[:, :1].cuda(), starts, o=o[:12])
         torch.cuda.synchronize()
         assert (o[12:] == 0).all()
+
+
+def test_unordered_starts_of_divided_sequences(gpu_lib):
+    """Starts that make more rows than there are: no part lies past the partials' memory."""
+    T = 300
+    cache, row, _ = shared_pages(64, 1, 2000, 16, False, 3)
+    q = ref.bf16(gen("unordered").standard_normal((T, 8, 64)))
+    for B in (3, 100):
+        table = row.expand(B, -1).contiguous()
+        lens = torch.full((B,), 2000, dtype=torch.int32, device="cuda")
+        for high in (T, 1 << 30):
+            starts = torch.tensor([0 if b % 2 else high for b in range(B + 1)], dtype=torch.int32, device="cuda")
+            o = torch.zeros(T + 2, 8, 64, dtype=torch.bfloat16, device="cuda")
+            gpu_lib.paged_chunk_attention(q.cuda(), *cache, table, lens, starts, o=o[:T])
+            torch.cuda.synchronize()
+            assert (o[T:] == 0).all()
 
 
 def test_two_streams_and_two_graphs(gpu_lib):
