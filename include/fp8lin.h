@@ -524,8 +524,8 @@ fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache
  *   q [T,Hq,D], k, v [T,Hkv,D] bf16  by strides in values (token, head; a head's D
  *                                    values lie together): views of a QKV projection
  *                                    will do.  Strides are multiples of 8, a token's
- *                                    0 .. 2^24, a head's 0 .. 2^36; Hq a multiple of Hkv: query head n reads key
- *                                    head n / (Hq / Hkv)
+ *                                    0 .. 2^24, a head's 0 .. 2^36; Hq a multiple of
+ *                                    Hkv: query head n reads key head n / (Hq / Hkv)
  *   starts [B+1] int32               prompt b is rows starts[b] .. starts[b+1] - 1:
  *                                    nondecreasing, 0 .. T (others are clamped: such
  *                                    prompts' rows are unspecified); 4-byte aligned
@@ -566,7 +566,9 @@ fp8l_status prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_
  * tokens up to its own (with window > 0 the last `window` of them).  A place below 0 (more
  * tokens than seq_lens[b]) sees nothing: o = 0 and lse = -inf.  Cache lines that no
  * token of the call sees may hold anything.  Everything else is as in
- * prompt_attention, page numbers as in paged_decode_attention.
+ * prompt_attention, page numbers as in paged_decode_attention.  A batch of up to 256
+ * sequences is divided by its lengths: a row's rounding depends on the lengths beside it
+ * too.
  */
 fp8l_status paged_chunk_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                                   const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,

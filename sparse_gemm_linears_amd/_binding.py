@@ -513,8 +513,8 @@ def prompt_attention(q, k, v, starts, scale=None, softcap: float = 0.0, window: 
                      return_lse: bool = False, o=None, lse=None):
     """Attention of packed prompts over their own keys: q [T,Hq,D], k and v [T,Hkv,D] bf16 (strided views will do, the
     values of a head together), prompt b in rows starts[b] .. starts[b+1]-1 (int32 [B+1]).  scale: D^-0.5 by default;
-    softcap > 0 caps the scores; causal: a token sees its prompt up to itself, with window > 0 the last `window` tokens of
-    that, otherwise all of its prompt.  Rows outside every prompt are left as they were.  Returns o [T,Hq,D] bf16, or
+    softcap > 0 caps the scores; causal: a token sees its prompt up to itself, with window > 0 the last `window` tokens
+    of that, otherwise all of its prompt.  Rows outside every prompt are left as they were.  Returns o [T,Hq,D] bf16, or
     (o, lse [T,Hq] fp32)."""
     return _marshal_module().prompt(q, k, v, starts, scale, softcap, window, causal, return_lse, o, lse, _stream_of(q))
 

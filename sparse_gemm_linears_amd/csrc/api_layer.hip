@@ -1,8 +1,8 @@
 // C entry points of the decoder-layer operators: the residual norm with e4m3
-// output, the rotary append to a paged cache and the attention over it.  The
-// checks run in the order of api.hip: shapes (an empty call returns here),
-// NULL pointers, alignment, aliasing, device; then scratch memory; then the
-// launches.
+// output, the rotary append to a paged cache and the attention over it, of one
+// token or several, or of prompts over their own keys.  The checks run in the
+// order of api.hip: shapes (an empty call returns here), NULL pointers,
+// alignment, aliasing, device; then scratch memory; then the launches.
 #include <cmath>
 
 #include "api_common.hpp"

@@ -9,7 +9,9 @@
 // cache, 189 MB in 33.8 us, 5.6 TB/s.  One token is bound by two memory
 // latencies and the launch: 3.0 us.  (Times in this file: one call of a replayed graph of
 // twelve over three sets of inputs in turn.  Issued one by one, calls take 37.5 and
-// 5.3 us.)
+// 5.3 us.)  With the norms and the keys kept in bf16 the 8192 tokens move 206 MB in 43.3 us, issued one by
+// one (4.8 TB/s; 37.5 without), one token takes 5.4 to 5.7 us: the norm adds 16 products and a sum over
+// a head's lanes to each head, which the loads in flight cover.
 #include <type_traits>
 
 #include "device_common.hpp"

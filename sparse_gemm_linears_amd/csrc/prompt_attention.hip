@@ -12,9 +12,19 @@
 // and one of these heads (row = token * group + head), so that a block of rows reads each
 // key once for all of them and a short chunk still fills a wave's rows.
 //
-// A wave holds 32 rows, a workgroup of 1 to 4 waves 32 to 128; tiles of 64 keys (32 for
-// D = 256) go through LDS, copied past the registers while the tile before is used, two
-// buffers each.  Layouts (v_mfma_f32_32x32x16_bf16: lane l, n = l % 32, h = l / 32):
+// A workgroup of four waves takes a block of up to 128 rows of one sequence and key head and goes
+// over the keys that some row of it sees, in tiles of 64 (32 for D = 256) that are copied to LDS
+// past the registers while the tile before is used, two buffers each.  How the waves share a
+// tile depends on the block's rows:
+//   more than 64   a wave holds 32 rows and takes all keys of a tile;
+//   33 to 64       two waves hold the same 32 rows and take half of a tile's keys each;
+//   at most 32 (a short sequence over a cache)   all four hold the rows, and each goes over tiles of
+//                  32 keys of its own without a barrier, codes converted as they are read: such
+//                  blocks wait for the cache alone (256-wide bf16 heads, whose tiles of four
+//                  waves LDS does not hold, go as the first).
+// Waves with the same rows add their states up through LDS at the end.
+//
+// Layouts (v_mfma_f32_32x32x16_bf16: lane l, n = l % 32, h = l / 32):
 //   scores   A = K: row n is key n, B = Q: column n is a row; lane half h holds values
 //            16 s + 8 h .. + 7 of step s;
 //   weights  the scores come out with column n = row and register i = key
@@ -25,11 +35,24 @@
 //            of 16 values; lane i gets value i of the four).
 // The weights enter the second product as one bf16 each (2^-9 relative, as much as the
 // output's own rounding when one key counts, and less the more there are); sums of
-// weights are of the fp32 values.
+// weights are of the fp32 values.  The reference of a row's exponents moves only when a score passes
+// it by 2^8, so that most tiles need no exchange between lanes and no correction of o.
 //
 // LDS rows are whole lines of a head; 16-byte chunks of a row are permuted by key_swizzle
 // and value_swizzle so that 16 rows of one column of K, and 8 rows of four columns
-// of V, lie in different banks.
+// of V, lie in different banks (no conflict counted over 8192 tokens).
+//
+// Measured (32 / 8 heads of 128): a prompt of 8192 tokens 537 to 567 us, 1.0 PFLOP/s, as the clock
+// allows (one bf16 product of 8192^3 reaches 1.25 to 1.36); 2048 tokens over 32768 1040 to
+// 1066 us, 1.0 PFLOP/s.  The matrix units are busy half of the time there, the
+// vector units 0.47 of it (exponentials, maxima, packing), two workgroups to a compute unit so that one's exponentials
+// overlap the other's products.  Level or slower at the long prompt: the next tile's scores
+// between the exponentials of this one (583 us against 537), three waves a SIMD with tiles of 32 keys (578 against
+// 565), blocks of 64 rows (676 against 566), blocks of 256 whose two halves take turns at products and
+// exponentials (580 against 569), wave priorities.  Few rows: 32 sequences of 5 to
+// 8192 tokens, 4 new ones each, e4m3, 190 MB in 55 to 58 us: 3.4 TB/s, the start of a part (5 us) and the
+// join (7 us) included.  Heads of 256 reach 0.94 PFLOP/s over 8192 tokens, of 64 0.75 to 0.79: half the
+// products for as many exponentials.
 #include <cmath>
 #include <type_traits>
 
@@ -134,7 +157,6 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-
 // Finds block `number` of the batch; false if the number is not used.
 __device__ __forceinline__ bool find_block(const PromptArgs &a, int64_t number, int tile, Block &k) {
   const int lane = threadIdx.x & 63, group = a.Hq / a.Hkv;
@@ -233,7 +255,9 @@ __device__ __forceinline__ bool find_share(const PromptArgs &a, const PromptPlan
   auto parts_of = [&](int j, float inverse) FP8LIN_INLINE {
     return min(max((int)__builtin_ceilf((float)cost[j] * inverse), 1), kMost);
   };
-  auto count_of = [&](int j, float inverse) FP8LIN_INLINE { return min(min(blocks[j], kMost) * parts_of(j, inverse), 1 << 20); };
+  auto count_of = [&](int j, float inverse) FP8LIN_INLINE {
+    return min(min(blocks[j], kMost) * parts_of(j, inverse), 1 << 20);
+  };
   auto large = [&](int j) FP8LIN_INLINE { return tokens[j] * (int64_t)group > kWaveRows; };
   auto mine_of = [&](float inverse, bool larges, bool others) FP8LIN_INLINE {
     int mine = 0;
@@ -347,7 +371,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     const int64_t number = plan.blocks - 1 - (int)(rest / (uint32_t)plan.splits);  // a sequence's longest rows first
     const bool ranked = !kPaged && a.causal && a.window == 0 && a.B > 1 && a.B <= 64 && plan.splits == 1;
     if (!(ranked ? find_ranked(a, (int)rest, KT, blk) : find_block(a, number, KT, blk))) return;
-    mine_part = Part{plan.per, (int)(rest % (uint32_t)plan.splits), plan.splits, (number * a.Hkv + kvh) * plan.splits, 1};
+    mine_part = Part{plan.per, (int)(rest % (uint32_t)plan.splits), plan.splits,
+                     (number * a.Hkv + kvh) * plan.splits, 1};
   }
   const int split = mine_part.split, tile0 = split * mine_part.per, tile_end = min(blk.tiles, tile0 + mine_part.per);
   if (split > 0 && tile0 >= blk.tiles) return;
@@ -381,8 +406,10 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
 
   v8bf qf[kHeld];
   auto load_queries = [&]() FP8LIN_INLINE {
-    const uint16_t *src = a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head;
-    const int first = kFp8 && few ? 16 * h : 8 * h, odd_step = kFp8 && few ? 8 : 16;  // few_key_frags' order, or key_frag's
+    const uint16_t *src =
+        a.q + (int64_t)(blk.start + token) * a.q_token + (int64_t)(kvh * group + row % group) * a.q_head;
+    // the order of few_tiles' raw codes, or key_frag's
+    const int first = kFp8 && few ? 16 * h : 8 * h, odd_step = kFp8 && few ? 8 : 16;
     // the weights' exponents grow with the scores: a negative scale turns the queries over
     const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
@@ -536,8 +563,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   // of the place that nothing else has.
   const int key_at = (32 * half + n) * kRow + 16 * key_swizzle<D>(n, h);
   const int value_r = 4 * h + (lane & 15) / 4;
-  const int value_at = (32 * half + value_r) * kRow + 16 * value_swizzle<D>(value_r, 2 * (lane >> 4 & 1) + (lane & 3) / 2) +
-                       8 * (lane & 1);
+  const int value_at = (32 * half + value_r) * kRow + 8 * (lane & 1) +
+                       16 * value_swizzle<D>(value_r, 2 * (lane >> 4 & 1) + (lane & 3) / 2);
   auto key_frag = [&](const uint8_t *lk, int at, int sub, int s) FP8LIN_INLINE {
     const uint4 raw = *reinterpret_cast<const uint4 *>(lk + (at ^ 32 * s) + 32 * sub * kRow);
     return as_bf16x8(raw.x, raw.y, raw.z, raw.w);
@@ -754,8 +781,9 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       const int key0 = blk.begin + t * KT, mine = key0 + 32 * half;
       bool odd = false;
       if (key0 + KT > block_end || key0 < block_low) odd = take_odd(lv, kOdd);
+      const bool edge = mine + kMine > all_end || mine < all_low;
       if (working && mine < any_end && mine + kMine > any_low)
-        use_tile(subs, mine, lk, lv, ls + 32 * half, ls + KT + 32 * half, mine + kMine > all_end || mine < all_low, odd);
+        use_tile(subs, mine, lk, lv, ls + 32 * half, ls + KT + 32 * half, edge, odd);
     };
     if (tile0 < tile_end) {
       fetch(tile0, lds_k0, lds_v0);
@@ -769,7 +797,9 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   // Blocks of at most 32 rows.  A wave's tile of 32 keys lies in LDS as it lies in memory (codes
   // become bf16 when they are read: no other wave reads them); the copies of the next
   // tile are under way while one is used, and no wave waits for another.
-  auto raw_swizzle = [&](int r, int c) FP8LIN_INLINE { return c ^ (D == 64 ? r >> 2 & 3 : D == 128 ? r >> 1 & 7 : r & 15); };
+  auto raw_swizzle = [&](int r, int c) FP8LIN_INLINE {
+    return c ^ (D == 64 ? r >> 2 & 3 : D == 128 ? r >> 1 & 7 : r & 15);
+  };
   auto few_tiles = [&]() FP8LIN_INLINE {
     constexpr int kFewCopies = 32 / kCopyRows, kLoads = 2 * kFewCopies + (kFp8 ? 1 : 0);
     const int key_begin = blk.begin + tile0 * KT, key_end = min(blk.end, blk.begin + tile_end * KT);
