@@ -195,6 +195,15 @@ __device__ __forceinline__ int wave_sum(int v) {
   return from_lane(v, 0) + from_lane(v, 16) + from_lane(v, 32) + from_lane(v, 48);
 }
 
+// Largest over the wave's 64 lanes of values that are not negative, in every lane.
+__device__ __forceinline__ int wave_max(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false));  // half mirror
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, false));  // mirror
+  return max(max(from_lane(v, 0), from_lane(v, 16)), max(from_lane(v, 32), from_lane(v, 48)));
+}
+
 // The block at `rank` of up to 64 prompts' blocks in falling order of their place in their
 // prompt: the ones with the most keys begin first, and the short ones fill the end.  (Seven
 // prompts of 131 to 1357 tokens of 28 heads of 64: 36 us with one prompt after the
@@ -266,10 +275,20 @@ __device__ __forceinline__ bool find_share(const PromptArgs &a, const PromptPlan
       if (j < each && (large(j) ? larges : others)) mine += count_of(j, inverse);
     return mine;
   };
-  constexpr int kLeast = 6;  // two tiles
-  int bound = kLeast - 1;    // the largest that is too small
-  for (int bit = 1 << (31 - __builtin_clz(3 * plan.per | 1)); bit > 0; bit >>= 1)
-    if (wave_sum(mine_of(__builtin_amdgcn_rcpf((float)(bound + bit)), true, true)) > plan.shares) bound += bit;
+  int most = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; j++) most = max(most, cost[j]);
+  most = wave_max(most);
+  // Two tiles at least, and as much as makes joining the longest sequence's parts (0.25 us each)
+  // cost no more than going over them does.
+  int bound = max(6, (int)__builtin_amdgcn_sqrtf((float)most)) - 1;  // the largest that is too small, or is not tried
+  auto too_many = [&](int x) FP8LIN_INLINE {
+    return wave_sum(mine_of(__builtin_amdgcn_rcpf((float)x), true, true)) > plan.shares;
+  };
+  if (too_many(bound + 1)) {
+    for (int bit = 1 << (31 - __builtin_clz(most | 1)); bit > 0; bit >>= 1)
+      if (too_many(bound + bit)) bound += bit;
+  }
   const float inverse = __builtin_amdgcn_rcpf((float)(bound + 1));
   const int mine_large = mine_of(inverse, true, false), all_large = wave_sum(mine_large);
   const bool takes_large = rank < all_large;  // the blocks that take longest begin first

@@ -61,9 +61,9 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   const int64_t found = (int64_t)p.blocks * a.Hkv;
   p.filled = rows <= p.blocks ? 1 : (int)(rows / p.blocks);
   int64_t splits = 1;
-  if (a.block_table && a.B > 1 && a.B <= kShareBatch && found <= 8 * cus && tiles > 2) {
-    // As many parts as run at once, or twice or three times as many where there are more blocks: a few
-    // more than run at once take longest.  (32 sequences of 5 to 8192 tokens, 16 rows each, e4m3, 8 key
+  if (a.block_table && a.B > 1 && a.B <= kShareBatch && found <= 8 * cus && tiles > 4) {
+    // As many parts as run at once, or a multiple of it where there are more blocks: a few more than run
+    // at once take longest.  (32 sequences of 5 to 8192 tokens, 16 rows each, e4m3, 8 key
     // heads: 64 parts a head 58 us, 72 70, 128 66, 192 75; of equal lengths 52 with 64, and 67 in 8 parts
     // each.)  Where some blocks are large they come first, and small ones fill the end.  (512 tokens over 4096
     // beside 23 single ones over 300 to 4096: 64 parts a head 113 us, 80 99, 96 108.)
@@ -74,18 +74,30 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     return p;
   }
   if (p.filled <= 64) {
-    // Small blocks are bound by the cache's bytes and by a workgroup's start; lengths differ, and what
-    // is cut evens them out.  (32 sequences of 5 to 8192 tokens, 16 rows each in e4m3: in 2, 4, 7, 8,
-    // 11, 14 parts 86, 87, 66, 76, 70, 70 us)
-    splits = (int64_t)2 * cus * (p.filled <= 32 ? 4 : 2) / found;
-    if (splits > tiles / 2) splits = tiles / 2;
-    if (splits < 1) splits = 1;
+    // Small blocks: a part takes its start and 1.3 us for each tile, or 1.7 for two of an e4m3 cache
+    // (whose tiles four waves hold at once, not two), and a division the second kernel and 0.25 us for
+    // each part that it joins.  (In us, 1 new token, 32 / 8 heads of 128 in bf16: over 777 in 7 parts 10.7; over
+    // 1500 in 12 12.2, in 5 14.4; over 8000 in 14, 42 and 63 20.9, 22.3 and 25.0; over 256 whole 10.3, in 2
+    // 10.1; over 384 13.0 and 10.2; in e4m3 over 448 whole 12.8, in 4 10.6.)
+    const int64_t each = a.k_scale && p.filled <= kWaveRows ? 2 : 1;
+    const double step = a.k_scale ? 1.7 : 1.3;
+    double best = 0;
+    for (int64_t s = 1; s == 1 || (s <= 64 && s <= tiles && s * found <= 8 * cus); s++) {
+      const int64_t per = (tiles + s - 1) / s, parts = found * s;
+      const int64_t rounds = (parts + 2 * cus - 1) / (2 * cus);
+      double us = rounds * (5 + (per + each - 1) / each * step);
+      if (s > 1) us += 2.5 + s * 0.25;
+      if (s == 1 || us < best) {
+        best = us;
+        splits = s;
+      }
+    }
   } else {
     // Large blocks: a tile takes a workgroup that has its compute unit alone about 0.7 of the time
     // that it takes two that share one; a part costs its start and its partials, and any division
     // the second kernel.  (In us, 32 / 8 heads of 128: 512 tokens over 4096 70 whole, 56 in 4 parts;
-    // prompts of 500 and of 1000 tokens
-    // 22 and 36 in 4 and 2 parts, 18 and 30 whole.)
+    // prompts of 500 and of 1000 tokens 22 and 36 in 4 and 2 parts, 18 and 30 whole; 20 tokens over 512
+    // 16.9 whole, 11.4 in 4.)
     const int64_t real = a.B == 1 ? (rows + kBlockRows - 1) / kBlockRows : rows / kBlockRows + (a.B + 1) / 2;
     const double codes = a.k_scale ? 1.5 : 1.0;
     const double alone = codes * (a.D == 64 ? 0.9 : 1.5), pair = codes * (a.D == 64 ? 1.4 : a.D == 128 ? 2.1 : 2.3);
@@ -97,7 +109,7 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
       const int64_t per = (usual + s - 1) / s, parts = real * a.Hkv * s;
       const int64_t rounds = parts <= cus ? 1 : (parts + 2 * cus - 1) / (2 * cus);
       double us = rounds * (5 + per * (parts <= cus ? alone : pair));
-      if (s > 1) us += 8 + s * 0.25 + parts * p.filled * (a.D + 2) * 8 / 8e6;
+      if (s > 1) us += 4 + s * 0.25 + parts * p.filled * (a.D + 2) * 8 / 8e6;
       if (s == 1 || us < best) {
         best = us;
         splits = s;
