@@ -66,6 +66,7 @@ namespace fp8lin {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLarge = 0x1p26f;  // of exponents, see weigh
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -98,6 +99,12 @@ __device__ __forceinline__ const char *scalar(const char *p) {
 __device__ __forceinline__ int opaque(int x) {
   asm volatile("" : "+v"(x));
   return x;
+}
+
+// a * b, rounded by itself.
+__device__ __forceinline__ float product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
 }
 
 // Neither loads nor anything else is moved past this place.
@@ -654,22 +661,33 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
     float top = x[0];
 #pragma unroll
     for (int j = 1; j < 16 * S; j++) top = fmaxf(top, x[j]);
-    top *= rate;
+    top = product(top, rate);
     // The reference of the exponents follows the maximum only when some score passes it by
     // 2^8: weights stay below 2^8 and sums far below overflow, and most tiles need no
-    // exchange between the lane halves and no product with the factor.
-    if (__any(top > (m == -INFINITY ? -INFINITY : m + 8.f))) {
+    // exchange between the lane halves and no product with the factor.  The reference is a rounded
+    // product: from 2^26 on an exact one may lie far from it (all weights would be 0, or infinite), and
+    // the products are rounded as it was.
+    float factor = rate;
+    bool rounded = false;
+    if (__any(top > (fabsf(m) < kLarge ? m + 8.f : -INFINITY))) {
       top = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)), m);
       const float shrink = top == m ? 1.f : __builtin_amdgcn_exp2f(m - top);
       m = top;
       l *= shrink;
 #pragma unroll
       for (int i = 0; i < D / 32; i++) o[i] *= shrink;
+      const float large = m == -INFINITY ? 0.f : m;
+      rounded = __any(fabsf(large) >= kLarge);
+      if (__builtin_expect(rounded, 0)) {
+        factor = 1.f;
+#pragma unroll
+        for (int j = 0; j < 16 * S; j++) x[j] = product(x[j], rate) - large;
+      }
     }
     before();
-    const float base = m == -INFINITY ? 0.f : m;
+    const float base = rounded || m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int j = 0; j < 16 * S; j++) x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], rate, -base));
+    for (int j = 0; j < 16 * S; j++) x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], factor, -base));
     {
       float sum[4] = {};
 #pragma unroll
