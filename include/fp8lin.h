@@ -531,7 +531,8 @@ fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache
  *                                    prompts' rows are unspecified); 4-byte aligned
  *   scale, softcap, window           score = scale (q . k); with softcap > 0,
  *                                    softcap tanh(score / softcap); |scale| <= 2^100, 0 <=
- *                                    softcap < inf, window >= 0
+ *                                    softcap < inf (more than 2^126 |scale| counts as
+ *                                    that), window >= 0
  *   causal                           not 0: token i sees tokens 0 .. i of its prompt, with
  *                                    window > 0 the last `window` of them; 0: all
  *                                    tokens of its prompt (window must be 0)

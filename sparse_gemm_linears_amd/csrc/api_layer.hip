@@ -150,11 +150,18 @@ fp8l_status prompt(PromptArgs a, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, 
   a.Hkv = (int)Hkv;
   a.D = (int)D;
   a.window = (int)(window < kMaxTokens ? window : kMaxTokens);
-  // a smaller cap has no reciprocal, and leaves scores that no exponential tells from 0 either
-  if (a.softcap > 0.0f && a.softcap < 1e-30f) a.softcap = 1e-30f;
-  if (a.softcap > 1e38f) a.softcap = 1e38f;  // log2(e) times it is finite; scores are as good as without one either way
   // scores of a scale of 0 are 0 under any cap; without one 0 times the -infinity of a hidden key would be a NaN
-  if (a.scale == 0.0f && a.softcap == 0.0f) a.softcap = 1.0f;
+  if (a.scale == 0.0f) a.softcap = 1.0f;
+  if (a.softcap > 0.0f) {
+    // The kernel multiplies q.k by scale / softcap, which has to be a normal number.  A smaller cap than
+    // 2^-127 |scale| (2^-27 at most) leaves scores that no exponential tells from 0 either, nor does one below
+    // 1e-30; a larger one than 2^126 |scale| is as good as none while |q.k| < 2^113.
+    const float size = std::fabs(a.scale);
+    if (a.softcap > 1e38f) a.softcap = 1e38f;  // log2(e) times it is finite
+    if (a.softcap * 0x1p-126f > size) a.softcap = size * 0x1p126f;
+    const float least = size * 0x1p-127f > 1e-30f ? size * 0x1p-127f : 1e-30f;
+    if (a.softcap < least) a.softcap = least;
+  }
   CallScratch sc;
   if (hipError_t e = sc.acquire(prompt_partial_bytes(a, device_cu_count()), 0, stream)) return launched(e);
   const hipError_t e = launch_prompt_attention(a, sc.partials(), stream);
