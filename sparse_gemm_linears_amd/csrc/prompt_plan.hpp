@@ -30,6 +30,9 @@ struct PromptPlan {
 // Sequences of a batch that shares are made for: four a lane.
 constexpr int kShareBatch = 256;
 
+// Most bytes of partials that a division leaves.
+constexpr int64_t kMostPartialBytes = 300000000;
+
 // Workgroups of one launch: a grid counts its threads in 32 bits.
 constexpr int kPromptGrid = 1 << 22;
 
@@ -61,14 +64,20 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
   const int64_t found = (int64_t)p.blocks * a.Hkv;
   p.filled = rows <= p.blocks ? 1 : (int)(rows / p.blocks);
   int64_t splits = 1;
-  if (a.block_table && a.B > 1 && a.B <= kShareBatch && found <= 8 * cus && tiles > 4) {
+  // Workgroups whose partials kMostPartialBytes holds, and the most that an even division makes: eight a
+  // compute unit.
+  const int64_t held = kMostPartialBytes / (prompt_part_floats(a.D) * (int64_t)sizeof(float));
+  const int64_t most = 8 * cus < held ? 8 * cus : held;
+  if (a.block_table && a.B > 1 && a.B <= kShareBatch && found <= most && tiles > 4) {
     // As many parts as run at once, or a multiple of it where there are more blocks: a few more than run
     // at once take longest.  (32 sequences of 5 to 8192 tokens, 16 rows each, e4m3, 8 key
     // heads: 64 parts a head 58 us, 72 70, 128 66, 192 75; of equal lengths 52 with 64, and 67 in 8 parts
     // each.)  Where some blocks are large they come first, and small ones fill the end.  (512 tokens over 4096
     // beside 23 single ones over 300 to 4096: 64 parts a head 113 us, 80 99, 96 108.)
     const int64_t round = 2 * cus, rounds = (found + found / 4 + round - 1) / round;
-    p.shares = (int)(rounds * round * (p.filled > kWaveRows ? 5 : 4) / 4 / a.Hkv);
+    // (up to 12.5 workgroups a compute unit; fewer of 256-wide heads, by their partials' bytes)
+    const int64_t all = rounds * round * (p.filled > kWaveRows ? 5 : 4) / 4;
+    p.shares = (int)((all < held ? all : held) / a.Hkv);
     p.splits = 1;
     p.per = (int)tiles;
     return p;
@@ -82,7 +91,7 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     const int64_t each = a.k_scale && p.filled <= kWaveRows ? 2 : 1;
     const double step = a.k_scale ? 1.7 : 1.3;
     double best = 0;
-    for (int64_t s = 1; s == 1 || (s <= 64 && s <= tiles && s * found <= 8 * cus); s++) {
+    for (int64_t s = 1; s == 1 || (s <= 64 && s <= tiles && s * found <= most); s++) {
       const int64_t per = (tiles + s - 1) / s, parts = found * s;
       const int64_t rounds = (parts + 2 * cus - 1) / (2 * cus);
       double us = rounds * (5 + (per + each - 1) / each * step);
@@ -104,8 +113,7 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     // (of packed prompts only the sum of their lengths is known: twice the mean stands for the longest)
     const int64_t mean = 2 * (int64_t)a.T / a.B / tile + 1, usual = a.block_table || tiles < mean ? tiles : mean;
     double best = 0;
-    // (no division makes more than eight workgroups a compute unit: its partials stay below 300 MB)
-    for (int64_t s = 1; s == 1 || (s <= 64 && s <= tiles && s * found <= 8 * cus); s++) {
+    for (int64_t s = 1; s == 1 || (s <= 64 && s <= tiles && s * found <= most); s++) {
       const int64_t per = (usual + s - 1) / s, parts = real * a.Hkv * s;
       const int64_t rounds = parts <= cus ? 1 : (parts + 2 * cus - 1) / (2 * cus);
       double us = rounds * (5 + per * (parts <= cus ? alone : pair));
