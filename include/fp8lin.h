@@ -527,8 +527,9 @@ fp8l_status paged_decode_attention_fp8(const uint16_t *q, const uint8_t *k_cache
  *                                    0 .. 2^24, a head's 0 .. 2^36; Hq a multiple of
  *                                    Hkv: query head n reads key head n / (Hq / Hkv)
  *   starts [B+1] int32               prompt b is rows starts[b] .. starts[b+1] - 1:
- *                                    nondecreasing, 0 .. T (others are clamped: such
- *                                    prompts' rows are unspecified); 4-byte aligned
+ *                                    nondecreasing, 0 .. T (others are clamped: every
+ *                                    row of o and lse is then unspecified, and
+ *                                    nothing else is written); 4-byte aligned
  *   scale, softcap, window           score = scale (q . k); with softcap > 0,
  *                                    softcap tanh(score / softcap); |scale| <= 2^100, 0 <=
  *                                    softcap < inf (more than 2^126 |scale| counts as

@@ -335,7 +335,9 @@ __device__ __forceinline__ bool find_share(const PromptArgs &a, const PromptPlan
   part.per = max(1, (k.tiles + splits - 1) / splits);
   part.slot = (int64_t)(rank - part.split) * a.Hkv + kvh;
   part.step = a.Hkv;
-  return rank - part.split + splits <= plan.shares;  // (not so of starts that are out of order)
+  // The block's parts have slots rank - split .. rank - split + splits - 1 (split <= index <= rank): all of
+  // them lie in the partials' memory.  (Starts that are out of order may make more.)
+  return rank - part.split + splits <= plan.shares;
 }
 
 // tanh of each value.  tanh z = 1 - 2 / (1 + exp 2z), but below 1/4, where that would lose a
