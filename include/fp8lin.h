@@ -568,9 +568,13 @@ fp8l_status prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_
  * tokens up to its own (with window > 0 the last `window` of them).  A place below 0 (more
  * tokens than seq_lens[b]) sees nothing: o = 0 and lse = -inf.  Cache lines that no
  * token of the call sees may hold anything.  Everything else is as in
- * prompt_attention, page numbers as in paged_decode_attention.  A batch of up to 256
- * sequences is divided by its lengths: a row's rounding depends on the lengths beside it
- * too.
+ * prompt_attention, page numbers as in paged_decode_attention.
+ * A batch of 2 to 256 sequences is divided by its lengths where ((T Hq / Hkv) / 128 + B) Hkv is at
+ * most eight for each compute unit (4 new tokens each, 32 query heads on 8 key heads, 256 compute
+ * units: up to 228 sequences): a row's rounding depends on the lengths beside it too.  Larger
+ * batches are divided evenly, by max_len, or not at all, so that one long sequence among
+ * many short ones takes about as long as it takes undivided: give it a call of its own.  A single
+ * sequence is divided by max_len too, not by its length: give the least bound that is known.
  */
 fp8l_status paged_chunk_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                                   const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,

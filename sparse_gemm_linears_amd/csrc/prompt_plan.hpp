@@ -74,6 +74,10 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     // heads: 64 parts a head 58 us, 72 70, 128 66, 192 75; of equal lengths 52 with 64, and 67 in 8 parts
     // each.)  Where some blocks are large they come first, and small ones fill the end.  (512 tokens over 4096
     // beside 23 single ones over 300 to 4096: 64 parts a head 113 us, 80 99, 96 108.)
+    // Larger batches fill the device whole: of lengths that spread they lose nothing, but one long sequence among
+    // short ones is then a single workgroup's for each key head.  (4 tokens each, e4m3, 8 key heads: 228
+    // sequences of 300 to 4096 210 us divided, 229 188 whole; with one of 32768 among at most 300 93 and 483.  256
+    // sequences on 2 key heads, one long: 58 us, 257: 917.)
     const int64_t round = 2 * cus, rounds = (found + found / 4 + round - 1) / round;
     // (up to 12.5 workgroups a compute unit; fewer of 256-wide heads, by their partials' bytes)
     const int64_t all = rounds * round * (p.filled > kWaveRows ? 5 : 4) / 4;
