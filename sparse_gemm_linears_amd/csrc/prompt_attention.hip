@@ -18,10 +18,13 @@
 // tile depends on the block's rows:
 //   more than 64   a wave holds 32 rows and takes all keys of a tile;
 //   33 to 64       two waves hold the same 32 rows and take half of a tile's keys each;
-//   at most 32 (a short sequence over a cache)   all four hold the rows, and each goes over tiles of
-//                  32 keys of its own without a barrier, codes converted as they are read: such
-//                  blocks wait for the cache alone (256-wide bf16 heads, whose tiles of four
-//                  waves LDS does not hold, go as the first).
+//   at most 32 (a short sequence over a cache)   as many waves as LDS has tiles for (four over e4m3
+//                  heads of 64 and 128, two over bf16 ones and e4m3 heads of 256) hold the rows, and
+//                  each goes over tiles of 32 keys of its own without a barrier, codes
+//                  converted as they are read: such blocks wait for the cache alone.  The other
+//                  waves have no work.
+// 256-wide heads know the first form, and over e4m3 the last: of up to 32 rows over a bf16 cache one wave
+// computes and all four copy.
 // Waves with the same rows add their states up through LDS at the end.
 //
 // Layouts (v_mfma_f32_32x32x16_bf16: lane l, n = l % 32, h = l / 32):
@@ -33,9 +36,13 @@
 //            keys are counted in that order;
 //   values   A = V transposed, read from LDS by ds_read_b64_tr_b16 (16 lanes take 4 keys
 //            of 16 values; lane i gets value i of the four).
-// The weights enter the second product as one bf16 each (2^-9 relative, as much as the
-// output's own rounding when one key counts, and less the more there are); sums of
-// weights are of the fp32 values.  The reference of a row's exponents moves only when a score passes
+// The weights enter the second product as one bf16 each (2^-8 of a weight at most): for values of
+// either sign that adds about as much to o as its own rounding does, over few keys or many.
+// Sums of weights are of the fp32 values.  A second product for the low halves takes a third of
+// the matrix rate of large blocks; small ones have the rate, but not the time for the halves
+// (in us, as it is and with them: 32 sequences of 5 to 8192 tokens, 4 new ones each, e4m3, 56.1
+// and 58.7, heads of 64 41.1 and 44.0, of 256 156 and 165; 256 single tokens 200 and 217).
+// paged_decode_attention has them.  The reference of a row's exponents moves only when a score passes
 // it by 2^8, so that most tiles need no exchange between lanes and no correction of o.
 //
 // LDS rows are whole lines of a head; 16-byte chunks of a row are permuted by key_swizzle
@@ -375,8 +382,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
   constexpr bool kPaged = SRC != Source::kRows, kFp8 = SRC == Source::kCodes;
   constexpr int KT = tile_keys(D), WAVES = kBlockWaves, kRow = 2 * D;  // bytes of an LDS row
   __shared__ __align__(1024) uint8_t lds_k0[KT * kRow], lds_k1[KT * kRow], lds_v0[KT * kRow], lds_v1[KT * kRow];
-  // waves of a block of at most 32 rows, each with tiles of 32 keys of its own
   constexpr int kBytes = kFp8 ? 1 : 2, kLine = D * kBytes;  // of a value and a cache line in memory
+  // waves of a block of at most 32 rows that work, each on tiles of 32 keys of its own
   constexpr int kFewTile = 32 * kLine, kFewWaves = KT * kRow / kFewTile < WAVES ? KT * kRow / kFewTile : WAVES;
   __shared__ __align__(16) float lds_s0[kFp8 ? 64 * WAVES : 1], lds_s1[kFp8 ? 64 * WAVES : 1];
   constexpr int kOddKeys = 32 * kFewWaves > KT ? 32 * kFewWaves : KT;
@@ -833,7 +840,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       if (t + 1 < tile_end) step(t + 1, std::true_type{});
     }
   };
-  // Blocks of at most 32 rows.  A wave's tile of 32 keys lies in LDS as it lies in memory (codes
+  // Blocks of at most 32 rows, over a cache.  A wave's tile of 32 keys lies in LDS as it lies in memory (codes
   // become bf16 when they are read: no other wave reads them); the copies of the next
   // tile are under way while one is used, and no wave waits for another.
   auto raw_swizzle = [&](int r, int c) FP8LIN_INLINE {
@@ -849,23 +856,19 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void prompt_kernel(PromptArgs 
       constexpr bool kKeys = decltype(keys)::value;
       return kFp8 ? raw_swizzle(r, c) : kKeys ? key_swizzle<D>(r, c) : value_swizzle<D>(r, c);
     };
-    int64_t runs = 0;  // of a cache: lane x holds the line of run x % 2 of the wave's tile 32 j + x / 2
+    int64_t runs = 0;  // lane x holds the line of run x % 2 of the wave's tile 32 j + x / 2
     auto fetch = [&](int i, uint8_t *lk, uint8_t *lv, float *ls) FP8LIN_INLINE {
       const int key0 = key_of(i);
-      if constexpr (kPaged) {
-        if (i % 32 == 0) {
-          const int key = key_of(i + (lane >> 1)) + 16 * (lane & 1);
-          if (key < blk.end) {
-            const int p = (int)((uint32_t)key / (uint32_t)a.page_size);
-            const int page = min(max(a.block_table[(int64_t)blk.b * a.max_pages + p], 0), a.pages - 1);
-            runs = ((int64_t)page * a.Hkv + kvh) * a.page_size + (key - p * a.page_size);
-          }
+      if (i % 32 == 0) {
+        const int key = key_of(i + (lane >> 1)) + 16 * (lane & 1);
+        if (key < blk.end) {
+          const int p = (int)((uint32_t)key / (uint32_t)a.page_size);
+          const int page = min(max(a.block_table[(int64_t)blk.b * a.max_pages + p], 0), a.pages - 1);
+          runs = ((int64_t)page * a.Hkv + kvh) * a.page_size + (key - p * a.page_size);
         }
       }
       const bool full = key0 >= blk.lowest && key0 + 32 <= blk.end;
-      auto line_of = [&](int run) FP8LIN_INLINE -> int64_t {
-        return kPaged ? from_lane(runs, 2 * (i % 32) + run) : (int64_t)blk.start + key0 + 16 * run;
-      };
+      auto line_of = [&](int run) FP8LIN_INLINE { return from_lane(runs, 2 * (i % 32) + run); };
       auto copy = [&](auto keys, int j, const char *base, int64_t line, uint8_t *to) FP8LIN_INLINE {
         const int r0 = j * kCopyRows;  // and rl: a copy's rows differ from the first one's by whole bits
         const int flip = place(keys, r0, 0);
