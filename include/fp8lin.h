@@ -455,7 +455,9 @@ fp8l_status kv_rope_append_fp8(const uint16_t *qkv, const int32_t *positions, co
  *                                  the whole head; NULL: those heads are not normed.
  *                                  0 <= eps < inf.  The squares are summed in fp32:
  *                                  where their sum passes its range the head's
- *                                  finite values become 0
+ *                                  finite values become 0, and where eps and all the
+ *                                  squares lie below it (eps 0 and |x| below 2^-75)
+ *                                  they become infinities, or a NaN of 0
  *   k_out [T, Hkv, D] bf16         keys of every token after norm and rotation, or
  *                                  NULL
  * Everything else, the limits included, is as in kv_rope_append; norm and rotation
@@ -575,6 +577,9 @@ fp8l_status prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_
  * batches are divided evenly, by max_len, or not at all, so that one long sequence among
  * many short ones takes about as long as it takes undivided: give it a call of its own.  A single
  * sequence is divided by max_len too, not by its length: give the least bound that is known.
+ * Partials of a divided call take up to 300 MB of scratch memory (128 rows for each part, whatever a
+ * block holds), which a captured graph keeps.  For one new token of every sequence
+ * paged_decode_attention is faster and more exact.
  */
 fp8l_status paged_chunk_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                                   const int32_t *block_table, const int32_t *seq_lens, const int32_t *starts,

@@ -38,8 +38,8 @@ EXPORTS = ("fp8_quant_act", "fp8_quant_weight_block", "prune24_compress", "fp8_b
            "fp8_grouped_gemm", "fp8_block_gemm_swiglu", "fp8_block_linear", "fp8_sparse24_linear",
            "fp8_quant_act_tensor", "fp8_quant_act_static", "fp8_quant_weight_tensor", "prune24_compress_tensor",
            "fp8_block_gemm_noalloc", "fp8_add_rmsnorm", "fp8_add_rmsnorm_ue8m0", "kv_rope_append",
-           "kv_rope_append_fp8", "kv_norm_rope_append", "kv_norm_rope_append_fp8", "paged_decode_attention", "paged_decode_attention_fp8",
-           "prompt_attention", "paged_chunk_attention", "paged_chunk_attention_fp8",
+           "kv_rope_append_fp8", "kv_norm_rope_append", "kv_norm_rope_append_fp8", "paged_decode_attention",
+           "paged_decode_attention_fp8", "prompt_attention", "paged_chunk_attention", "paged_chunk_attention_fp8",
            "fp8lin_release_graph_scratch", "fp8lin_status_str")
 MAX_LINEAR_M = 64  # the fused-quantization calls take decode-sized batches
 

@@ -51,15 +51,19 @@
 //
 // Measured (32 / 8 heads of 128): a prompt of 8192 tokens 537 to 567 us, 1.0 PFLOP/s, as the clock
 // allows (one bf16 product of 8192^3 reaches 1.25 to 1.36); 2048 tokens over 32768 1040 to
-// 1066 us, 1.0 PFLOP/s.  The matrix units are busy half of the time there, the
+// 1100 us, 1.0 PFLOP/s (e4m3 1594 us, 0.67).  The matrix units are busy half of the time there, the
 // vector units 0.47 of it (exponentials, maxima, packing), two workgroups to a compute unit so that one's exponentials
 // overlap the other's products.  Level or slower at the long prompt: the next tile's scores
 // between the exponentials of this one (583 us against 537), three waves a SIMD with tiles of 32 keys (578 against
 // 565), blocks of 64 rows (676 against 566), blocks of 256 whose two halves take turns at products and
 // exponentials (580 against 569), wave priorities.  Few rows: 32 sequences of 5 to
 // 8192 tokens, 4 new ones each, e4m3, 190 MB in 55 to 58 us: 3.4 TB/s, the start of a part (5 us) and the
-// join (7 us) included.  Heads of 256 reach 0.94 PFLOP/s over 8192 tokens, of 64 0.75 to 0.79: half the
-// products for as many exponentials.
+// join (7 us) included.  Heads of 256 reach 0.94 to 1.0 PFLOP/s over 8192 tokens, of 64 0.75 to 0.87: half
+// the products for as many exponentials.
+//
+// Registers: the forms of 256-wide heads have all 256 in use and spill, 66 to 71 vector registers over an
+// e4m3 cache (124 to 152 bytes a lane), 2 to 4 over a bf16 one and for capped rows.  The e4m3 forms of
+// 64 and 128 keep 183 to 205 scalar registers in lanes of vector ones.
 #include <cmath>
 #include <type_traits>
 
@@ -254,7 +258,7 @@ struct Part {
 // The part at `rank` of a key head's, where long sequences are divided most: into as many
 // parts as keep every one's cost below the least bound for which all parts are at most
 // plan.shares.  A tile of a block of at most 32 rows counts as two thirds of another one in e4m3
-// (which waits for the cache), and one and a half times as much in bf16.
+// (which waits for the cache), and one and a half times as much in bf16 (measured with heads of 128).
 template <bool CODES>
 __device__ __forceinline__ bool find_share(const PromptArgs &a, const PromptPlan &plan, int rank, int kvh, int tile,
                                            Block &k, Part &part) {

@@ -91,7 +91,10 @@ inline PromptPlan plan_prompt(const PromptArgs &a, int cus) {
     // (whose tiles four waves hold at once, not two), and a division the second kernel and 0.25 us for
     // each part that it joins.  (In us, 1 new token, 32 / 8 heads of 128 in bf16: over 777 in 7 parts 10.7; over
     // 1500 in 12 12.2, in 5 14.4; over 8000 in 14, 42 and 63 20.9, 22.3 and 25.0; over 256 whole 10.3, in 2
-    // 10.1; over 384 13.0 and 10.2; in e4m3 over 448 whole 12.8, in 4 10.6.)
+    // 10.1; over 384 13.0 and 10.2; in e4m3 over 448 whole 12.8, in 4 10.6.)  The rates are of heads of
+    // 128, and serve the others: of 1 to 64 parts for 1 and 12 new tokens over 384 to 8000, in both types,
+    // the choice is within 10 % of the best for heads of 64 (384 keys in 6 parts 10.1, whole 9.3), 6 % for 128,
+    // and 13 % for 256 (12 tokens over 8000 in bf16 in 36 parts 33.7, in 32 29.9).
     const int64_t each = a.k_scale && p.filled <= kWaveRows ? 2 : 1;
     const double step = a.k_scale ? 1.7 : 1.3;
     double best = 0;
